@@ -9,6 +9,10 @@ library is missing or fails to load, every call raises.
     out     = recurrent_step(q, k, v, log_alpha, beta, state, scale)   # state in place
     maps, offs = chunk_fwd_segmap(q, k, v, log_alpha, beta)            # context parallelism
     start   = affine_prefix(maps, offs, h0)
+    out, hT = glr_scan_fwd(x, log_a, h0=None, cu_seqlens=None)         # elementwise recurrence
+    out     = tree_fwd(q, k, v, log_alpha, beta, state, parents, scale)  # drafted tokens
+    state   = tree_commit(k, v, log_alpha, beta, state, parents, accepted)
+    y       = group_norm_fwd(x, weight, gate=z, activation="sigmoid")  # output norm and gate
 """
 import ctypes
 import os
@@ -17,6 +21,8 @@ import torch
 
 __all__ = ["chunk_fwd", "recurrent_step", "gdn_chunk_fwd", "gdn_recurrent_step", "KDAError",
            "chunk_fwd_segmap", "affine_prefix", "chunk_bwd", "gdn_chunk_bwd",
+           "glr_scan_fwd", "glr_scan_bwd", "glr_step", "tree_fwd", "tree_commit",
+           "group_norm_fwd", "group_norm_bwd", "GLR_TILE", "TREE_MAX_NODES",
            "library_path", "version",
            "profiler_enable", "profiler_read",
            "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA",
@@ -27,6 +33,10 @@ KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_NO_MEMOR
 _IO = {torch.float32: 0, torch.bfloat16: 1}
 _IMPL = {"auto": 0, "simt": 1, "tensorcore": 2, "tensorcore_chain": 3,
          "tensorcore_segmented": 4, "tensorcore_fused": 5}
+
+_ACT = {"none": 0, "sigmoid": 1, "silu": 2}
+GLR_TILE = 64           # tokens between the states that glr_scan_fwd keeps for the backward
+TREE_MAX_NODES = 64     # drafted tokens per sequence
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -85,6 +95,20 @@ def _load():
     lib.kda_debug_prep_image.restype = ctypes.c_int
     lib.kda_debug_bounded_wait.argtypes = [ctypes.c_int32, vp, vp]
     lib.kda_debug_bounded_wait.restype = ctypes.c_int
+    lib.kda_glr_scan_fwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.c_int, vp]
+    lib.kda_glr_scan_fwd_slots.argtypes = [vp] * 7 + [i64] * 4 + [ctypes.c_int, vp]
+    lib.kda_glr_scan_bwd.argtypes = [vp] * 10 + [i64] * 3 + [ctypes.c_int, vp]
+    lib.kda_glr_step.argtypes = [vp] * 4 + [i64] * 2 + [ctypes.c_int, vp]
+    lib.kda_glr_step_slots.argtypes = [vp] * 5 + [i64] * 3 + [ctypes.c_int, vp]
+    lib.kda_tree_fwd.argtypes = [vp] * 10 + [i64] * 6 + [ctypes.c_float, ctypes.c_int, vp]
+    lib.kda_tree_commit.argtypes = [vp] * 8 + [i64] * 6 + [ctypes.c_int, vp]
+    norm = [i64] * 3 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_int, vp]
+    lib.kda_group_norm_fwd.argtypes = [vp] * 5 + norm
+    lib.kda_group_norm_bwd.argtypes = [vp] * 9 + norm
+    for fn in (lib.kda_glr_scan_fwd, lib.kda_glr_scan_fwd_slots, lib.kda_glr_scan_bwd,
+               lib.kda_glr_step, lib.kda_glr_step_slots, lib.kda_tree_fwd, lib.kda_tree_commit,
+               lib.kda_group_norm_fwd, lib.kda_group_norm_bwd):
+        fn.restype = ctypes.c_int
     lib.kda_workspace_high_water.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.c_int]
     lib.kda_workspace_high_water.restype = ctypes.c_int
     lib.kda_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
@@ -401,6 +425,243 @@ def gdn_chunk_bwd(q, k, v, log_a, beta, scale, dout, h0=None, dhT=None, cu_seqle
     with one gate per (token, head), log_a [B,T,H] fp32; returns dlog_a [B,T,H]."""
     return chunk_bwd(q, k, v, log_a, beta, scale, dout, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens,
                      need_dh0=need_dh0, _gdn=True)
+
+
+def _call(name, dev, *args):
+    """Calls a C entry point on ``dev``'s current stream, with ``dev`` current; tensors in
+    ``args`` become their device addresses.  Raises KDAError on a failed status."""
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device, not {dev}")
+    fn = getattr(_lib or _load(), name)
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != KDA_OK:
+        raise KDAError(st, name)
+
+
+def _io_code(x):
+    if x.dtype not in _IO:
+        raise TypeError(f"unsupported I/O dtype {x.dtype}")
+    return _IO[x.dtype]
+
+
+def _offsets(cu_seqlens, rows, dev):
+    """Number of sequences of a call, after checking cu_seqlens (None: one per row)."""
+    if cu_seqlens is None:
+        return rows
+    if rows != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.device != dev \
+            or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a 1-D contiguous int32 tensor of N + 1 >= 2 offsets on "
+                         "the same device, and the other tensors have a leading axis of 1")
+    return cu_seqlens.numel() - 1
+
+
+def glr_scan_fwd(x, log_a, h0=None, cu_seqlens=None, out=None, hT=None, output_final_state=True,
+                 state_pool=None, slots=None, output_starts=False):
+    """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t per channel (C ABI
+    ``kda_glr_scan_fwd``, or ``kda_glr_scan_fwd_slots`` when ``slots`` is given).
+
+    x [B,T,D] in fp32 or bf16; log_a [B,T,D] fp32, <= 0; h0 [N,D] fp32 or None.
+    ``cu_seqlens``, ``slots`` and ``state_pool`` [P,D] as for :func:`chunk_fwd`.
+    Returns (out [B,T,D], hT [N,D] fp32 or None; with slots: state_pool in hT's place),
+    and with ``output_starts`` a third tensor, the states that :func:`glr_scan_bwd`
+    starts from ([B, ceil(T/GLR_TILE), D] fp32)."""
+    if x.dim() != 3:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [B, T, D]")
+    B, T, D = x.shape
+    dev, io = x.device, _io_code(x)
+    _check(x, "x", x.dtype, x.shape, dev)
+    _check(log_a, "log_a", torch.float32, x.shape, dev)
+    N = _offsets(cu_seqlens, B, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.dtype, x.shape, dev)
+    starts = torch.empty((B, -(-T // GLR_TILE), D), dtype=torch.float32, device=dev) \
+        if output_starts else None
+    if slots is not None:
+        if state_pool is None or h0 is not None or hT is not None:
+            raise ValueError("slots go with state_pool (and without h0 / hT)")
+        _check(slots, "slots", torch.int32, (N,), dev)
+        P = state_pool.shape[0]
+        _check(state_pool, "state_pool", torch.float32, (P, D), dev)
+        _call("kda_glr_scan_fwd_slots", dev, x, log_a, state_pool, slots, out, starts, cu_seqlens,
+              N, T, P, D, io)
+        hT = state_pool
+    else:
+        if state_pool is not None:
+            raise ValueError("state_pool goes with slots")
+        if h0 is not None:
+            _check(h0, "h0", torch.float32, (N, D), dev)
+        if hT is not None:
+            _check(hT, "hT", torch.float32, (N, D), dev)
+        elif output_final_state:
+            hT = torch.empty((N, D), dtype=torch.float32, device=dev)
+        _call("kda_glr_scan_fwd", dev, x, log_a, h0, out, hT, starts, cu_seqlens, N, T, D, io)
+    return (out, hT, starts) if output_starts else (out, hT)
+
+
+def glr_scan_bwd(x, log_a, dout, starts=None, h0=None, dhT=None, cu_seqlens=None, need_dh0=True):
+    """Gradients of sum(dout * out) + sum(dhT * hT) for :func:`glr_scan_fwd` on the same
+    inputs (C ABI ``kda_glr_scan_bwd``).  ``starts`` as glr_scan_fwd returned it with
+    ``output_starts``; None recomputes it.  Returns (dx in the I/O dtype, dlog_a fp32,
+    dh0 [N,D] fp32 or None)."""
+    if x.dim() != 3:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [B, T, D]")
+    B, T, D = x.shape
+    dev, io = x.device, _io_code(x)
+    _check(x, "x", x.dtype, x.shape, dev)
+    _check(log_a, "log_a", torch.float32, x.shape, dev)
+    _check(dout, "dout", x.dtype, x.shape, dev)
+    N = _offsets(cu_seqlens, B, dev)
+    if starts is not None:
+        _check(starts, "starts", torch.float32, (B, -(-T // GLR_TILE), D), dev)
+    for name, t in (("h0", h0), ("dhT", dhT)):
+        if t is not None:
+            _check(t, name, torch.float32, (N, D), dev)
+    dx, dlog_a = torch.empty_like(x), torch.empty_like(log_a)
+    dh0 = torch.empty((N, D), dtype=torch.float32, device=dev) if need_dh0 else None
+    _call("kda_glr_scan_bwd", dev, x, log_a, h0, starts, dout, dhT, dx, dlog_a, dh0, cu_seqlens,
+          N, T, D, io)
+    return dx, dlog_a, dh0
+
+
+def glr_step(x, log_a, state, out=None, slots=None):
+    """One token per sequence of the gated linear recurrence (C ABI ``kda_glr_step``):
+    x, log_a [N,D]; ``state`` [N,D] fp32 is updated in place.  With ``slots`` (int32 [N]
+    on the device) ``state`` is a pool [P,D] (``kda_glr_step_slots``).  Returns out [N,D]."""
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [N, D]")
+    N, D = x.shape
+    dev, io = x.device, _io_code(x)
+    _check(x, "x", x.dtype, x.shape, dev)
+    _check(log_a, "log_a", torch.float32, x.shape, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.dtype, x.shape, dev)
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (N,), dev)
+        P = state.shape[0]
+        _check(state, "state", torch.float32, (P, D), dev)
+        _call("kda_glr_step_slots", dev, x, log_a, state, slots, out, N, P, D, io)
+    else:
+        _check(state, "state", torch.float32, (N, D), dev)
+        _call("kda_glr_step", dev, x, log_a, state, out, N, D, io)
+    return out
+
+
+def _tree_args(k, v, log_alpha, beta, state, parents, slots):
+    """Shapes that tree_fwd and tree_commit share: (N, P, K, H, dk, dv, device, io code)."""
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k and v: expected [N, K, H, d]")
+    N, K, H, dk = k.shape
+    dv = v.shape[-1]
+    dev, io = k.device, _io_code(k)
+    _check(k, "k", k.dtype, k.shape, dev)
+    _check(v, "v", k.dtype, (N, K, H, dv), dev)
+    _check(log_alpha, "log_alpha", torch.float32, k.shape, dev)
+    _check(beta, "beta", torch.float32, (N, K, H), dev)
+    _check(parents, "parents", torch.int32, (N, K), dev)
+    P = N
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (N,), dev)
+        P = state.shape[0]
+    _check(state, "state", torch.float32, (P, H, dk, dv), dev)
+    return N, P, K, H, dk, dv, dev, io
+
+
+def tree_fwd(q, k, v, log_alpha, beta, state, parents, scale, num_nodes=None, slots=None, out=None):
+    """Outputs of a tree of drafted tokens over each sequence's cached state, which is
+    read and not written (C ABI ``kda_tree_fwd``).
+
+    q, k [N,K,H,dk], v [N,K,H,dv] in fp32 or bf16 for up to TREE_MAX_NODES nodes per
+    sequence; log_alpha [N,K,H,dk], beta [N,K,H] fp32; ``state`` [N,H,dk,dv] fp32, or with
+    ``slots`` (int32 [N]) a pool [P,H,dk,dv]; ``parents`` int32 [N,K], each below its own
+    index or -1 for the cached state; ``num_nodes`` int32 [N] or None: nodes past it are
+    skipped and their rows of ``out`` left as they were.  Returns out [N,K,H,dv]."""
+    N, P, K, H, dk, dv, dev, io = _tree_args(k, v, log_alpha, beta, state, parents, slots)
+    _check(q, "q", k.dtype, k.shape, dev)
+    if num_nodes is not None:
+        _check(num_nodes, "num_nodes", torch.int32, (N,), dev)
+    if out is None:
+        # skipped rows of a fresh output are zero
+        out = (torch.empty if num_nodes is None else torch.zeros)((N, K, H, dv), dtype=k.dtype, device=dev)
+    else:
+        _check(out, "out", k.dtype, (N, K, H, dv), dev)
+    _call("kda_tree_fwd", dev, q, k, v, log_alpha, beta, state, slots, parents, num_nodes, out,
+          N, P, K, H, dk, dv, float(scale), io)
+    return out
+
+
+def tree_commit(k, v, log_alpha, beta, state, parents, accepted, slots=None):
+    """Applies the drafted tokens on the path to node ``accepted[n]`` (int32 [N]; -1: none)
+    to each sequence's state, in place (C ABI ``kda_tree_commit``).  Other arguments as
+    for :func:`tree_fwd`.  Returns ``state``."""
+    N, P, K, H, dk, dv, dev, io = _tree_args(k, v, log_alpha, beta, state, parents, slots)
+    _check(accepted, "accepted", torch.int32, (N,), dev)
+    _call("kda_tree_commit", dev, k, v, log_alpha, beta, state, slots, parents, accepted,
+          N, P, K, H, dk, dv, io)
+    return state
+
+
+def _norm_args(x, weight, bias, gate, activation):
+    """(M, G, d, 1 for weights of every head, io code) of a group norm's arguments."""
+    if x.dim() < 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [..., G, d]")
+    if activation not in _ACT:
+        raise ValueError(f"activation {activation!r}: expected one of {sorted(_ACT)}")
+    G, d = x.shape[-2:]
+    M = 1
+    for n in x.shape[:-2]:
+        M *= n
+    dev, io = x.device, _io_code(x)
+    _check(x, "x", x.dtype, x.shape, dev)
+    if gate is not None:
+        _check(gate, "gate", x.dtype, x.shape, dev)
+    lead = weight if weight is not None else bias
+    per_group = 1 if lead is not None and lead.dim() == 2 else 0
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(t, name, torch.float32, (G, d) if per_group else (d,), dev)
+    return M, G, d, per_group, io
+
+
+def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="sigmoid", center=False,
+                   out=None):
+    """Group norm over the last axis with an activation (C ABI ``kda_group_norm_fwd``): for
+    x [..., G, d], n = norm(x) * weight + bias over each head's d channels, then
+    n * act(gate), or act(n) when gate is None.  The norm is the RMS one, or with ``center``
+    the mean is subtracted first.  weight, bias fp32 [d] (shared) or [G,d], or None;
+    activation "none", "sigmoid" or "silu".  Returns out like x."""
+    M, G, d, per_group, io = _norm_args(x, weight, bias, gate, activation)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.dtype, x.shape, x.device)
+    _call("kda_group_norm_fwd", x.device, x, gate, weight, bias, out, M, G, d, per_group,
+          1 if center else 0, float(eps), _ACT[activation], io)
+    return out
+
+
+def group_norm_bwd(x, weight, dout, bias=None, gate=None, eps=1e-5, activation="sigmoid",
+                   center=False):
+    """Gradients of :func:`group_norm_fwd` on the same inputs for ``dout`` like x (C ABI
+    ``kda_group_norm_bwd``).  Returns (dx, dgate in the I/O dtype, dweight, dbias fp32); a
+    gradient whose input is None is None."""
+    M, G, d, per_group, io = _norm_args(x, weight, bias, gate, activation)
+    _check(dout, "dout", x.dtype, x.shape, x.device)
+    dx = torch.empty_like(x)
+    dgate = torch.empty_like(x) if gate is not None else None
+    dweight = torch.empty_like(weight) if weight is not None else None
+    dbias = torch.empty_like(bias) if bias is not None else None
+    _call("kda_group_norm_bwd", x.device, x, gate, weight, bias, dout, dx, dgate, dweight, dbias,
+          M, G, d, per_group, 1 if center else 0, float(eps), _ACT[activation], io)
+    return dx, dgate, dweight, dbias
 
 
 IMAGE_BYTES = 66560   # one (chunk, head) operand image of the tensor-core prefill

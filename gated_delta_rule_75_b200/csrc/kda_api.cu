@@ -91,23 +91,33 @@ static kda_status_t from_cuda(cudaError_t e)
     return KDA_ERR_CUDA;
 }
 
-// Stream-ordered allocation that is always released on scope exit.
-struct StreamBuffer {
-    void* ptr = nullptr;
-    cudaStream_t st = nullptr;
-    cudaError_t alloc(size_t bytes, cudaStream_t s) {
-        st = s;
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e) return e;
-        cudaMemPool_t pool = workspace_pool(dev);
-        if (!pool) return cudaErrorMemoryAllocation;
-        return cudaMallocFromPoolAsync(&ptr, bytes, pool, s);
+kda_status_t status_from_cuda(cudaError_t e) { return from_cuda(e); }
+
+kda_status_t finish_call(cudaError_t e, cudaStream_t st)
+{
+    if (e == cudaSuccess && debug_mode()) {
+        int flag = 0;
+        if ((e = take_error_word(st, &flag))) return from_cuda(e);
+        return status_from_error_bits(flag);
     }
-    ~StreamBuffer() {
-        if (ptr) cudaFreeAsync(ptr, st);
-    }
-};
+    return from_cuda(e);
+}
+
+cudaError_t StreamBuffer::alloc(size_t bytes, cudaStream_t s)
+{
+    st = s;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e) return e;
+    cudaMemPool_t pool = workspace_pool(dev);
+    if (!pool) return cudaErrorMemoryAllocation;
+    return cudaMallocFromPoolAsync(&ptr, bytes, pool, s);
+}
+
+StreamBuffer::~StreamBuffer()
+{
+    if (ptr) cudaFreeAsync(ptr, st);
+}
 
 }  // namespace kda
 

@@ -251,6 +251,14 @@ enum KernelId {
     K_BWD_DENSE2,
     K_BWD_PARAM,
     K_FUSED_TC,
+    K_GLR_FWD,
+    K_GLR_BWD,
+    K_GLR_STEP,
+    K_TREE_FWD,
+    K_TREE_COMMIT,
+    K_GNORM_FWD,
+    K_GNORM_BWD,
+    K_GNORM_WGRAD,
     K_KERNEL_COUNT
 };
 
@@ -334,6 +342,97 @@ kda_status_t status_from_error_bits(int bits);
 // KDA_DEBUG=1 in the environment (read once): every call waits for its stream and
 // returns the status of the error bits it finds (kda_api.cu).
 bool debug_mode_on();
+
+// kda_api.cu: stream-ordered workspace from the library's pool on the current
+// device, released (in stream order) on scope exit; the status of a CUDA error.
+struct StreamBuffer {
+    void* ptr = nullptr;
+    cudaStream_t st = nullptr;
+    StreamBuffer() = default;
+    StreamBuffer(const StreamBuffer&) = delete;
+    StreamBuffer& operator=(const StreamBuffer&) = delete;
+    cudaError_t alloc(size_t bytes, cudaStream_t s);
+    ~StreamBuffer();
+};
+kda_status_t status_from_cuda(cudaError_t e);
+// What an entry point returns after its launches: the launch status, or in debug
+// mode the status of the error bits found once `st` has finished.
+kda_status_t finish_call(cudaError_t e, cudaStream_t st);
+
+// Pointer checks of the entry points.
+inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// A required tensor: present and 16-byte aligned.
+inline bool tensor_ok(const void* p) { return p != nullptr && is_aligned(p, 16); }
+// An optional one: absent, or 16-byte aligned.
+inline bool optional_ok(const void* p) { return p == nullptr || is_aligned(p, 16); }
+// Whether [a, a + na) and [b, b + nb) share a byte (absent tensors share none).
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// Gated linear recurrence (kda_glr.cu).
+struct GlrArgs {
+    const void* x;
+    const float* log_a;
+    const float* h0;            // [N][D], the pool with slots, or null
+    float* hT;                  // [N][D], the pool with slots, or null
+    void* out;                  // null: only hT and starts are wanted
+    float* starts;              // [B][ceil(T / KDA_GLR_TILE)][D]; written by the forward, read by the backward
+    const int32_t* slots;       // [N] or null
+    int64_t P;                  // pool rows (with slots)
+    const int32_t* cu;          // [N + 1] or null
+    int64_t N, B, T, D;         // sequences; rows of the token axis (1 with cu), tokens a row, channels
+    const void* dout;           // backward only, from here
+    const float* dhT;
+    void* dx;
+    float* dlog_a;
+    float* dh0;
+    kda_io_dtype_t io;
+    int* err;
+};
+cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st);
+cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st);
+cudaError_t launch_glr_step(const void* x, const float* log_a, float* state, const int32_t* slots,
+                            void* out, int64_t N, int64_t P, int64_t D, kda_io_dtype_t io, int* err,
+                            cudaStream_t st);
+
+// Drafted token trees (kda_tree.cu).
+struct TreeArgs {
+    const void *q, *k, *v;
+    const float *log_alpha, *beta;
+    float* state;               // [P][H][dk][dv] with slots, else [N][H][dk][dv]
+    const int32_t* slots;       // [N] or null
+    const int32_t* parents;     // [N][K]
+    const int32_t* num_nodes;   // [N] or null (tree_fwd)
+    const int32_t* accepted;    // [N] (tree_commit)
+    void* out;
+    int64_t N, P, K, H;
+    int dk, dv;
+    float scale;
+    kda_io_dtype_t io;
+    int* err;
+};
+cudaError_t launch_tree_fwd(const TreeArgs& a, cudaStream_t st);
+cudaError_t launch_tree_commit(const TreeArgs& a, cudaStream_t st);
+
+// Group norm with an activation (kda_group_norm.cu).
+struct GroupNormArgs {
+    const void *x, *gate;       // [M][G][d]; gate may be null
+    const float *weight, *bias; // [d] or [G][d]; may be null
+    void* out;
+    const void* dout;           // backward only, from here
+    void *dx, *dgate;
+    float *dweight, *dbias;
+    int64_t M, G, d;
+    bool per_group, center;
+    float eps;
+    int act;
+    kda_io_dtype_t io;
+};
+cudaError_t launch_group_norm_fwd(const GroupNormArgs& a, cudaStream_t st);
+cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t st);
 
 // Self-test of the bounded mbarrier wait (kda_selftest.cu).
 cudaError_t launch_bounded_wait_selftest(int* err, uint32_t polls, cudaStream_t st);

@@ -402,6 +402,151 @@ KDA_API kda_status_t kda_affine_prefix(const float* maps, const float* offs, con
                                        int64_t dv, cudaStream_t stream);
 
 /*
+ * Gated linear recurrence: the elementwise sibling of the delta rule, with the same
+ * per-channel decay and a vector for a state.  The pages' per-token step ("Kimi
+ * Delta Attention: la atencion lineal detras de Kimi K2 y Qwen3", section "Como
+ * funciona Kimi Delta Attention paso a paso") without its key and value products;
+ * recurrent layers that stand beside KDA layers in a model use it:
+ *
+ *     h_t = exp(log_a_t) h_{t-1} + x_t          (per channel)
+ *
+ *  x, out      [B, T, D]  io_dtype
+ *  log_a       [B, T, D]  fp32, natural log of the decay, <= 0; -inf forgets the state
+ *  h0, hT      [N, D]     fp32 states before the first and after the last token, or NULL
+ *              (zeros; not written); hT may be h0
+ *  starts      [B, ceil(T / KDA_GLR_TILE), D] fp32 or NULL: written with the state
+ *              before tokens 0, KDA_GLR_TILE, 2 KDA_GLR_TILE, .. of every row (h0 of its
+ *              sequence where that token begins one), which the backward takes.
+ *              (A row of starts holds arbitrary values where malformed cu_seqlens leave
+ *              the token in no sequence.)
+ *  cu_seqlens  as for kda_chunk_fwd (x, log_a, out and starts then have a leading axis
+ *              of 1, B is the number of sequences, N = B)
+ * Any D >= 1 up to 2^20 (rows of D a multiple of 4 are moved in wide accesses); D, B
+ * or T of 0 is a no-op apart from hT = h0.  The state is fp32 throughout; out is
+ * rounded once.  A call over more than one tile of the token axis uses a workspace of
+ * about 9 bytes per tile and channel from the library's pool.  The result is the same
+ * on every run.
+ *
+ * kda_glr_scan_fwd_slots -- h0 = hT = state_pool[slots[n]] ([P, D] fp32), with the
+ *   rules of kda_chunk_fwd_slots: a negative slot starts from zero and stores nothing,
+ *   one >= P too (and sets bit 0 of the error word); two sequences must not share one.
+ * kda_glr_scan_bwd -- gradients of L = sum(dout * out) + sum(dhT * hT):
+ *     g_t = dout_t + exp(log_a_{t+1}) g_{t+1}  (+ dhT at the last token),
+ *     dx_t = g_t,  dlog_a_t = g_t exp(log_a_t) h_{t-1},  dh0 = exp(log_a_1) g_1.
+ *   starts as kda_glr_scan_fwd wrote it for the same x, log_a, h0 and cu_seqlens, or
+ *   NULL: the call then makes them by a forward pass into workspace (4 bytes per tile
+ *   and channel).  dout, dx io_dtype; dlog_a, dhT, dh0 fp32; dhT NULL for zero, dh0
+ *   NULL if not wanted; dh0 may be dhT.
+ * kda_glr_step -- one token per sequence: x, log_a, out [N, D], state [N, D] in place.
+ *   kda_glr_step_slots: state_pool [P, D]; a negative slot gives a zero output row.
+ * Outputs must not overlap inputs or one another except as stated.
+ */
+#define KDA_GLR_TILE 64
+KDA_API kda_status_t kda_glr_scan_fwd(const void* x, const float* log_a, const float* h0, void* out,
+                                      float* hT, float* starts, const int32_t* cu_seqlens,
+                                      int64_t B, int64_t T, int64_t D, kda_io_dtype_t io_dtype,
+                                      cudaStream_t stream);
+
+KDA_API kda_status_t kda_glr_scan_fwd_slots(const void* x, const float* log_a, float* state_pool,
+                                            const int32_t* slots, void* out, float* starts,
+                                            const int32_t* cu_seqlens, int64_t B, int64_t T,
+                                            int64_t P, int64_t D, kda_io_dtype_t io_dtype,
+                                            cudaStream_t stream);
+
+KDA_API kda_status_t kda_glr_scan_bwd(const void* x, const float* log_a, const float* h0,
+                                      const float* starts, const void* dout, const float* dhT,
+                                      void* dx, float* dlog_a, float* dh0, const int32_t* cu_seqlens,
+                                      int64_t B, int64_t T, int64_t D, kda_io_dtype_t io_dtype,
+                                      cudaStream_t stream);
+
+KDA_API kda_status_t kda_glr_step(const void* x, const float* log_a, float* state, void* out,
+                                  int64_t N, int64_t D, kda_io_dtype_t io_dtype, cudaStream_t stream);
+
+KDA_API kda_status_t kda_glr_step_slots(const void* x, const float* log_a, float* state_pool,
+                                        const int32_t* slots, void* out, int64_t N, int64_t P,
+                                        int64_t D, kda_io_dtype_t io_dtype, cudaStream_t stream);
+
+/*
+ * Speculative decoding: a tree of drafted tokens read over each sequence's cached
+ * state.  The pages name batched decode and state reuse as what serving has to get
+ * right ("Kimi Linear acaba de superar a la atencion completa en sus propios
+ * terminos", section on serving reliability); a recurrent state cannot be masked like
+ * a key cache, so a draft is checked without writing any state and the accepted path
+ * is applied afterwards.
+ *
+ * kda_tree_fwd -- outputs of every drafted node, as kda_recurrent_step would give them
+ *   after the tokens on the node's path; the states are read, not written.
+ *  q, k        [N, K, H, dk]  io_dtype, K <= KDA_TREE_MAX_NODES nodes per sequence
+ *  v           [N, K, H, dv]  io_dtype
+ *  log_alpha   [N, K, H, dk]  fp32;  beta [N, K, H] fp32
+ *  state       [N, H, dk, dv] fp32; with slots (DEVICE int32 [N]) a pool [P, H, dk, dv]:
+ *              a negative slot (or one >= P, reported in bit 0 of the error word) reads
+ *              a zero state.  Sequences may share a slot here.
+ *  parents     DEVICE int32 [N, K]: the node before this one, < the node's own index, or
+ *              -1 for the cached state (other values count as -1 and set bit 0)
+ *  num_nodes   DEVICE int32 [N] or NULL (all K): nodes past num_nodes[n] are not read and
+ *              their rows of out are left as they were (values outside [0, K] are clamped
+ *              and set bit 0)
+ *  out         [N, K, H, dv]  io_dtype
+ * kda_tree_commit -- applies the tokens on the path to node accepted[n] (DEVICE int32
+ *   [N]) to the sequence's state, in place; accepted[n] = -1, or a negative slot,
+ *   leaves the state as it is, and so does accepted[n] outside [-1, K) or a slot >= P
+ *   (bit 0).  The result is that of kda_recurrent_step on those tokens one by one.
+ *   Two sequences must not share a slot.
+ * Every decay factor enters as a product of factors <= 1, so both hold at any decay
+ * rate.  No workspace is used.
+ */
+#define KDA_TREE_MAX_NODES 64
+KDA_API kda_status_t kda_tree_fwd(const void* q, const void* k, const void* v, const float* log_alpha,
+                                  const float* beta, const float* state, const int32_t* slots,
+                                  const int32_t* parents, const int32_t* num_nodes, void* out,
+                                  int64_t N, int64_t P, int64_t K, int64_t H, int64_t dk, int64_t dv,
+                                  float scale, kda_io_dtype_t io_dtype, cudaStream_t stream);
+
+KDA_API kda_status_t kda_tree_commit(const void* k, const void* v, const float* log_alpha,
+                                     const float* beta, float* state, const int32_t* slots,
+                                     const int32_t* parents, const int32_t* accepted, int64_t N,
+                                     int64_t P, int64_t K, int64_t H, int64_t dk, int64_t dv,
+                                     kda_io_dtype_t io_dtype, cudaStream_t stream);
+
+/*
+ * Group norm with an activation, channels last: what a layer does to the mixer's
+ * output before its projection.  The groups are the heads; statistics run over one
+ * head's channels of one token:
+ *
+ *     n = (x - mean) / sqrt(mean((x - mean)^2) + eps) * weight + bias
+ *     out = n * act(gate),  or act(n) without a gate
+ *
+ * with the mean subtracted only when center != 0 (else the RMS form).
+ *  x, gate, out   [M, G, d] io_dtype (M = tokens, e.g. B * T); gate may be NULL
+ *  weight, bias   fp32, [d] shared by the heads, or [G, d] with per_group != 0; NULL for
+ *                 ones / zeros
+ *  eps            > 0
+ * 1 <= d <= 512, G <= 65535; out must not overlap the inputs.
+ * kda_group_norm_bwd -- gradients for dout [M, G, d]: dx and dgate (required exactly
+ *   when gate is given) in io_dtype; dweight, dbias fp32 in the layout of weight and
+ *   bias, or NULL if not wanted (dweight is also defined for weight NULL).  The sums over tokens
+ *   are fp32, in a fixed order (the same result on every run), through a workspace of at
+ *   most 16 MB.  M = 0 sets dweight and dbias to zero.
+ */
+typedef enum {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SIGMOID = 1,
+    KDA_ACT_SILU = 2           /* z * sigmoid(z) */
+} kda_activation_t;
+
+KDA_API kda_status_t kda_group_norm_fwd(const void* x, const void* gate, const float* weight,
+                                        const float* bias, void* out, int64_t M, int64_t G, int64_t d,
+                                        int per_group, int center, float eps, kda_activation_t act,
+                                        kda_io_dtype_t io_dtype, cudaStream_t stream);
+
+KDA_API kda_status_t kda_group_norm_bwd(const void* x, const void* gate, const float* weight,
+                                        const float* bias, const void* dout, void* dx, void* dgate,
+                                        float* dweight, float* dbias, int64_t M, int64_t G, int64_t d,
+                                        int per_group, int center, float eps, kda_activation_t act,
+                                        kda_io_dtype_t io_dtype, cudaStream_t stream);
+
+/*
  * kda_debug_prep_image -- test hook, not part of the method: runs only the
  * tensor-core prep kernel (cumulative decay and intra-chunk transform) of a
  * fixed-length bf16 batch with dk = dv = 128 and leaves its per-(chunk, head)

@@ -1,0 +1,213 @@
+"""Gated linear recurrence on the GPU against the fp64 recurrence, element by element: lengths
+from one token over tile borders to many tiles, packed sequences with empty ones, channel counts
+that no vector divides, pools, strong and no decay, gradients, refusals of the device."""
+import pytest
+import torch
+
+import operators_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kda(cuda_ok):
+    from gated_delta_rule_75_b200 import build
+    build.build()
+    import gated_delta_rule_75_b200 as kda
+    return kda
+
+
+def inputs(B, T, D, io, seed, N=None, decay="usual"):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g)
+    la = -torch.log1p(torch.exp(n(B, T, D) - 3))
+    if decay == "none":
+        la = torch.zeros(B, T, D)
+    elif decay == "strong":
+        la = -40 * torch.rand((B, T, D), generator=g)
+    elif decay == "forget":                                  # exp(-inf) = 0 here and there
+        la = torch.where(torch.rand((B, T, D), generator=g) < 0.1, torch.tensor(float("-inf")), la)
+    x = n(B, T, D).to(R.IO[io])
+    return x.cuda(), la.cuda(), n(N or B, D).cuda()
+
+
+def offsets(lens):
+    cu = [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    return cu, torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+def starts_of(H, h0, B, T, cu, tile):
+    """States before the first token of every tile."""
+    h0 = torch.zeros(B if cu is None else len(cu) - 1, H.shape[-1], dtype=torch.float64) if h0 is None else h0
+    out = torch.zeros(B, -(-T // tile), H.shape[-1], dtype=torch.float64)
+    for b, t0, t1, n in R.spans(B, T, cu):
+        for t in range(t0, t1):
+            if t % tile == 0:
+                out[b, t // tile] = h0[n] if t == t0 else H[b, t - 1]
+    return out
+
+
+FIXED = [(1, 1, 1), (2, 1, 7), (3, 63, 130), (2, 64, 64), (1, 65, 4), (2, 129, 33), (1, 500, 6), (5, 200, 260),
+         (1, 2500, 12), (1, 9001, 3)]
+PACKED = [([1], 5), ([3, 0, 1, 0, 60, 64, 65], 36), ([0, 0, 130], 7), ([200, 0, 0], 8), ([1] * 70, 4),
+          ([700, 1, 64, 128, 333], 132), ([5000, 0, 2111], 5)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", FIXED)
+def test_forward_and_backward_rows(kda, B, T, D, io):
+    x, la, h0 = inputs(B, T, D, io, 100 * T + D)
+    check(kda, x, la, h0, None, None)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,D", PACKED)
+def test_forward_and_backward_packed(kda, lens, D, io):
+    cu, dcu = offsets(lens)
+    x, la, h0 = inputs(1, cu[-1], D, io, 7 * cu[-1] + D, N=len(lens))
+    check(kda, x, la, h0, cu, dcu)
+
+
+@pytest.mark.parametrize("decay", ["none", "strong", "forget"])
+def test_decay_extremes(kda, decay):
+    x, la, h0 = inputs(2, 300, 40, "f32", 3, decay=decay)
+    check(kda, x, la, h0, None, None)
+    cu, dcu = offsets([129, 0, 400])
+    x, la, h0 = inputs(1, cu[-1], 24, "bf16", 4, N=3, decay=decay)
+    check(kda, x, la, h0, cu, dcu)
+
+
+def check(kda, x, la, h0, cu, dcu):
+    B, T, D = x.shape
+    H, hT, E, eT = R.glr(R.d(x), R.d(la), R.d(h0), cu)
+    out, last, starts = kda.glr_scan_fwd(x, la, h0=h0, cu_seqlens=dcu, output_starts=True)
+    R.within(out, H, E, "out")
+    R.within(last, hT, eT, "hT")
+    R.within(starts, starts_of(H, R.d(h0), B, T, cu, kda.GLR_TILE), starts_of(E, h0.cpu().double() * 0, B, T, cu, kda.GLR_TILE),
+             "starts")
+    again, _ = kda.glr_scan_fwd(x, la, h0=h0, cu_seqlens=dcu)
+    assert torch.equal(out, again)
+    g = torch.Generator().manual_seed(T + D)
+    dout = torch.randn((B, T, D), generator=g).to(x.dtype).cuda()
+    dhT = torch.randn(h0.shape, generator=g).cuda()
+    for first, seed in ((h0, dhT), (None, None)):
+        if first is None:
+            starts = None
+        dx, dla, dh0 = kda.glr_scan_bwd(x, la, dout, starts=starts, h0=first, dhT=seed, cu_seqlens=dcu)
+        want = R.glr_grads(R.d(x), R.d(la), R.d(first), R.d(dout), R.d(seed), cu)
+        R.within(dx, want[0], want[3], "dx")
+        R.within(dla, want[1], want[4], "dlog_a")
+        R.within(dh0, want[2], want[5], "dh0")
+    assert kda.glr_scan_bwd(x, la, dout, cu_seqlens=dcu, need_dh0=False)[2] is None
+
+
+def test_pool_chunked_scan_then_steps(kda):
+    """Prompts scanned in two pieces and then token by token, all through pool slots, one of them
+    without a state: every output equals the whole recurrence's."""
+    lens, D, P, cut, steps = [150, 64, 3], 20, 5, 70, 3
+    full = [n + steps for n in lens]
+    cu, _ = offsets(full)
+    x, la, h0 = inputs(1, cu[-1], D, "f32", 9, N=3)
+    slots = torch.tensor([4, -1, 0], dtype=torch.int32, device="cuda")
+    pool = torch.randn(P, D, device="cuda")
+    before = pool.clone()
+    pool[4], pool[0] = h0[0], h0[2]
+    first = R.d(h0)
+    first[1] = 0
+    H, hT, E, eT = R.glr(R.d(x), R.d(la), first, cu)
+
+    def part(pieces):
+        at = torch.cat([torch.arange(cu[n] + a, cu[n] + b) for n, (a, b) in enumerate(pieces)]).cuda()
+        _, seg = offsets([b - a for a, b in pieces])
+        return x[:, at].contiguous(), la[:, at].contiguous(), seg, at
+
+    a, b, seg, at = part([(0, min(cut, n)) for n in lens])
+    out, got = kda.glr_scan_fwd(a, b, cu_seqlens=seg, state_pool=pool, slots=slots)
+    assert got is pool
+    R.within(out[0], H[0, at.cpu()], E[0, at.cpu()], "first piece")
+    a, b, seg, at = part([(min(cut, n), n) for n in lens])
+    out, _ = kda.glr_scan_fwd(a, b, cu_seqlens=seg, state_pool=pool, slots=slots)
+    # the sequence without a slot has at most `cut` tokens: its second piece is empty
+    R.within(out[0], H[0, at.cpu()], E[0, at.cpu()], "second piece")
+    for s in range(steps):
+        at = torch.tensor([cu[n] + lens[n] + s for n in range(3)])
+        o = kda.glr_step(x[0, at].contiguous(), la[0, at].contiguous(), pool, slots=slots)
+        for n in (0, 2):
+            R.within(o[n], H[0, at[n]], E[0, at[n]], "step")
+        assert float(o[1].abs().max()) == 0
+    R.within(pool[4], hT[0], eT[0], "state 4")
+    R.within(pool[0], hT[2], eT[2], "state 0")
+    assert torch.equal(pool[1:4], before[1:4])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("N,D", [(1, 1), (3, 5), (7, 256), (130, 1030), (2, 4099)])
+def test_step(kda, N, D, io):
+    x, la, h = inputs(1, N, D, io, N + D, N=N)
+    state = h.clone()
+    out = kda.glr_step(x[0], la[0], state)
+    want, _, E, _ = R.glr(R.d(x).transpose(0, 1), R.d(la).transpose(0, 1), R.d(h))
+    R.within(out, want[:, 0], E[:, 0], "out")
+    R.within(state, want[:, 0], E[:, 0], "state")
+
+
+def test_state_in_place_and_no_states(kda):
+    x, la, h0 = inputs(2, 100, 12, "f32", 21)
+    _, want = kda.glr_scan_fwd(x, la, h0=h0)
+    buf = h0.clone()
+    _, got = kda.glr_scan_fwd(x, la, h0=buf, hT=buf)
+    assert got is buf and torch.equal(buf, want)
+    out, none = kda.glr_scan_fwd(x, la, output_final_state=False)
+    assert none is None
+    H, _, E, _ = R.glr(R.d(x), R.d(la), None)
+    R.within(out, H, E, "out")
+
+
+def test_no_tokens(kda):
+    x, la, h0 = inputs(2, 1, 8, "f32", 22)
+    out, hT, starts = kda.glr_scan_fwd(x[:, :0], la[:, :0], h0=h0, output_starts=True)
+    assert out.shape == (2, 0, 8) and starts.shape == (2, 0, 8) and torch.equal(hT, h0)
+    dx, dla, dh0 = kda.glr_scan_bwd(x[:, :0], la[:, :0], x[:, :0], h0=h0, dhT=h0)
+    assert dx.numel() == 0 and torch.equal(dh0, h0)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, hT = kda.glr_scan_fwd(x[:1, :0], la[:1, :0], h0=h0, cu_seqlens=cu)
+    assert torch.equal(hT, h0)
+    pool = h0.clone()
+    kda.glr_scan_fwd(x[:1, :0], la[:1, :0], cu_seqlens=cu, state_pool=pool,
+                     slots=torch.tensor([1, -1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(pool, h0)
+    assert kda.glr_step(x[0, :0].reshape(0, 8), la[0, :0].reshape(0, 8), h0[:0]).shape == (0, 8)
+
+
+def test_bad_slots_and_offsets_are_reported(kda):
+    x, la, _ = inputs(1, 100, 8, "f32", 23)
+    pool = torch.ones(2, 8, device="cuda")
+    _, cu = offsets([40, 60])
+    slots = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    with pytest.raises(kda.KDAError) as e:
+        kda.glr_scan_fwd(x, la, cu_seqlens=cu, state_pool=pool, slots=slots)
+    assert e.value.status == kda.KDA_ERR_INVALID_ARG and float(pool[1].min()) == 1
+    with pytest.raises(kda.KDAError):
+        kda.glr_step(x[0, :2], la[0, :2], pool, slots=slots)
+    for bad in ([0, 60, 40, 100], [1, 50, 100], [0, 50, 90], [0, -5, 100], [0, 120, 100]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        with pytest.raises(kda.KDAError) as e:
+            kda.glr_scan_fwd(x, la, cu_seqlens=cu)
+        assert e.value.status == kda.KDA_ERR_INVALID_ARG
+        with pytest.raises(kda.KDAError):
+            kda.glr_scan_bwd(x, la, x, cu_seqlens=cu)
+
+
+def test_not_a_number_stays_in_its_sequence_and_channel(kda):
+    cu, dcu = offsets([100, 200, 150])
+    x, la, h0 = inputs(1, 450, 8, "f32", 24, N=3)
+    x[0, 150, 3] = float("nan")
+    x[0, 20, 1] = float("inf")
+    out, hT = kda.glr_scan_fwd(x, la, h0=h0, cu_seqlens=dcu)
+    bad = ~torch.isfinite(out[0])
+    want = torch.zeros_like(bad)
+    want[150:300, 3] = True
+    want[20:100, 1] = True
+    assert torch.equal(bad, want) and int((~torch.isfinite(hT)).sum()) == 2

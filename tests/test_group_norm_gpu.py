@@ -1,0 +1,118 @@
+"""Group norm with an activation on the GPU against its fp64 form, element by element, and its
+gradients against reverse mode in fp64."""
+import pytest
+import torch
+
+import operators_ref as R
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def kda(cuda_ok):
+    from gated_delta_rule_75_b200 import build
+    build.build()
+    import gated_delta_rule_75_b200 as kda
+    return kda
+
+
+def inputs(M, G, d, io, per_group, seed, offset=0.0):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g)
+    shape = (G, d) if per_group else (d,)
+    t = lambda v: v.to(R.IO[io]).cuda()
+    return (t(n(M, G, d) + offset), t(n(M, G, d) * 2), (1 + 0.2 * n(*shape)).cuda(), (0.2 * n(*shape)).cuda(),
+            t(n(M, G, d)))
+
+
+SIZES = [(1, 1, 1), (3, 2, 5), (2, 3, 8), (7, 5, 32), (65, 1, 64), (33, 4, 128), (300, 16, 128), (10, 33, 100),
+         (9, 2, 250), (5, 3, 255), (4, 7, 512), (6, 1, 509), (2000, 3, 64), (1, 300, 128), (3, 700, 20)]
+FORMS = [("sigmoid", False, False, True, True, False), ("silu", True, True, True, True, True),
+         ("silu", False, True, False, True, False), ("none", True, False, False, False, True),
+         ("none", False, True, True, False, False)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("name,center,per_group,gated,weighted,biased", FORMS)
+@pytest.mark.parametrize("M,G,d", SIZES)
+def test_values_and_gradients(kda, M, G, d, name, center, per_group, gated, weighted, biased, io):
+    x, z, w, b, dy = inputs(M, G, d, io, per_group, M + 31 * G + d, offset=0.5 if center else 0.0)
+    z, w, b = z if gated else None, w if weighted else None, b if biased else None
+    kw = dict(eps=EPS, activation=name, center=center)
+    out = kda.group_norm_fwd(x, w, bias=b, gate=z, **kw)
+    form = lambda x, w, b, z: R.group_norm(x, w, b, z, EPS, name, center)
+    bound = R.group_norm_bound(R.d(x), R.d(w), R.d(b), R.d(z), EPS, name, center)
+    R.within(out, form(R.d(x), R.d(w), R.d(b), R.d(z)), bound, "out")
+    dx, dz, dw, db = kda.group_norm_bwd(x, w, dy, bias=b, gate=z, **kw)
+    want = R.grads(form, [R.d(t) for t in (x, w, b, z)], R.d(dy))
+    assert (dz is None) == (z is None) and (dw is None) == (w is None) and (db is None) == (b is None)
+    # magnitudes that the gradients sum, each off by a few ROW (its own rounding, the statistics', the
+    # activation's): 8 ROW of them bounds the error; sums over tokens add at most (tokens a slot, the slots,
+    # the rows) half steps, under 2^-12 of the magnitudes for these sizes even one after another
+    X = R.d(x)
+    mu = X.mean(-1, keepdim=True) if center else torch.zeros_like(X[..., :1])
+    r = 1 / torch.sqrt(((X - mu) ** 2).mean(-1, keepdim=True) + EPS)
+    xh = (X - mu) * r
+    big = (X.abs() + (X.abs().mean(-1, keepdim=True) if center else 0)) * r        # what xh is made of
+    big = big + big.mean(-1, keepdim=True) * xh.abs()
+    W = torch.ones(d).double() if w is None else R.d(w).abs()
+    nb = big * W + (0 if b is None else R.d(b).abs())
+    t = R.d(z) if gated else form(X, R.d(w), R.d(b), None) if name == "none" else \
+        R.group_norm(X, R.d(w), R.d(b), None, EPS, "none", center)
+    f, slope = R.act(name, t).abs(), 1.1
+    dn = R.d(dy).abs() * ((f + (0 if gated else slope)) if gated else slope * (1 + nb * (name != "none")))
+    c = dn * W
+    dx_big = r * (c + xh.abs() * (c * big).mean(-1, keepdim=True) + c.mean(-1, keepdim=True)) * (1 + big)
+    R.within(dx, want[0], 8 * R.ROW * dx_big, "dx")
+    if gated:
+        R.within(dz, want[3], 8 * R.ROW * R.d(dy).abs() * nb * slope, "dgate")
+    rows = 0 if per_group else (0, 1)
+    steps = (M * (1 if per_group else G) + 64) * 2.0 ** -24
+    if weighted:
+        R.within(dw, want[1], (8 * R.ROW + steps) * (dn * big).sum(rows), "dweight")
+    if biased:
+        R.within(db, want[2], (8 * R.ROW + steps) * dn.sum(rows), "dbias")
+    again = kda.group_norm_bwd(x, w, dy, bias=b, gate=z, **kw)
+    assert all(p is None or torch.equal(p, q) for p, q in zip((dx, dz, dw, db), again))
+
+
+def test_leading_axes_and_constant_rows(kda):
+    x, z, w, _, _ = inputs(12, 2, 64, "f32", False, 3)
+    a = kda.group_norm_fwd(x.view(3, 4, 2, 64), w, gate=z.view(3, 4, 2, 64))
+    assert torch.equal(a.view(12, 2, 64), kda.group_norm_fwd(x, w, gate=z))
+    x[:] = 5.0                                            # no variance: the centred norm is exactly zero
+    assert float(kda.group_norm_fwd(x, w, activation="none", center=True).abs().max()) == 0
+    x[:] = 0.0
+    assert float(kda.group_norm_fwd(x, w, activation="none").abs().max()) == 0
+
+
+def test_large_offset_loses_nothing_more(kda):
+    """A mean 1000 times the deviation: the error stays that of the inputs' own magnitude."""
+    x, _, w, b, _ = inputs(40, 3, 128, "f32", False, 5, offset=1000.0)
+    out = kda.group_norm_fwd(x, w, bias=b, activation="none", center=True)
+    want = R.group_norm(R.d(x), R.d(w), R.d(b), None, EPS, "none", True)
+    R.within(out, want, R.group_norm_bound(R.d(x), R.d(w), R.d(b), None, EPS, "none", True), "out")
+
+
+def test_extreme_gates_and_bad_rows(kda):
+    x, z, w, _, _ = inputs(6, 2, 32, "f32", False, 7)
+    z[0, 0] = float("inf")
+    z[1, 0] = -1e30
+    x[2, 1, 3] = float("nan")
+    out = kda.group_norm_fwd(x, w, gate=z, activation="sigmoid")
+    n = kda.group_norm_fwd(x, w, activation="none")
+    assert torch.equal(out[0, 0], n[0, 0]) and float(out[1, 0].abs().max()) == 0
+    bad = ~torch.isfinite(out)
+    assert bool(bad[2, 1].all()) and int(bad.sum()) == 32
+
+
+def test_no_rows(kda):
+    w = torch.ones(64, device="cuda")
+    x = torch.zeros(0, 4, 64, device="cuda")
+    assert kda.group_norm_fwd(x, w).shape == (0, 4, 64)
+    dx, _, dw, db = kda.group_norm_bwd(x, w, x, bias=w)
+    assert dx.shape == (0, 4, 64) and float(dw.abs().sum()) == 0 and float(db.abs().sum()) == 0
+    x = torch.zeros(3, 0, 64, device="cuda")
+    assert kda.group_norm_fwd(x, w).shape == (3, 0, 64)
