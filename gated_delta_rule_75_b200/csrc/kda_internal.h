@@ -331,7 +331,8 @@ cudaError_t run_prefill_fused(const PrefillArgs& a, int* err, int* ticket, const
 // 2, 3: its MMAs; 4: state-walk stage copies; 5: state-walk MMAs; 6: the state
 // walk's worker/issuer hand-offs).
 constexpr int kErrSeqlens = 1 << 0;
-constexpr int kErrTimeoutMask = 0x7e;
+constexpr int kErrScanWait = 1 << 7;   // gated linear recurrence: a tile's wait for the ones before it
+constexpr int kErrTimeoutMask = 0xfe;
 
 // kda_errors.cu: the library's per-GPU device error word (the current device's),
 // taking it (read and clear, ordered on `st`, waits for `st`), and the status its

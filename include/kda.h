@@ -436,7 +436,7 @@ KDA_API kda_status_t kda_affine_prefix(const float* maps, const float* offs, con
  *   starts as kda_glr_scan_fwd wrote it for the same x, log_a, h0 and cu_seqlens, or
  *   NULL: the call then makes them by a forward pass into workspace (4 bytes per tile
  *   and channel).  dout, dx io_dtype; dlog_a, dhT, dh0 fp32; dhT NULL for zero, dh0
- *   NULL if not wanted; dh0 may be dhT.
+ *   NULL if not wanted.
  * kda_glr_step -- one token per sequence: x, log_a, out [N, D], state [N, D] in place.
  *   kda_glr_step_slots: state_pool [P, D]; a negative slot gives a zero output row.
  * Outputs must not overlap inputs or one another except as stated.
@@ -592,6 +592,8 @@ KDA_API kda_status_t kda_debug_bounded_wait(int32_t polls, int32_t* err_word, cu
  *              operand MMAs, 4: state copies, 5: state-walk MMAs, 6: hand-offs
  *              between warps); the kernel stopped that work without faulting
  *              and its outputs are unspecified
+ *   bit 7      the same for a tile of the gated linear recurrence that waited for
+ *              the tiles before it
  * Returns KDA_ERR_INVALID_ARG for word == NULL, KDA_ERR_CUDA if a CUDA call
  * failed, KDA_OK otherwise.
  */

@@ -68,7 +68,7 @@ def test_scan_backward_argument_errors(lib):
         assert scan_bwd(lib, **{name: at(9, 4)}) == BAD, name
     assert scan_bwd(lib, dx=at(3)) == BAD and scan_bwd(lib, dg=at(1)) == BAD and scan_bwd(lib, dx=at(5)) == BAD
     assert scan_bwd(lib, dh0=at(6, 4)) == BAD and scan_bwd(lib, dh0=at(4)) == BAD
-    assert scan_bwd(lib, dhT=at(6), dh0=at(6, 128)) == BAD
+    assert scan_bwd(lib, dhT=at(6), dh0=at(6, 128)) == BAD and scan_bwd(lib, dhT=at(6), dh0=at(6)) == BAD
     assert scan_bwd(lib, cu=at(6), B=0) == BAD and scan_bwd(lib, B=0) == OK
 
 
