@@ -34,7 +34,7 @@ constexpr int kWarps = 8;
 constexpr int kSteps = kTile / kWarps;  // tokens of a warp
 constexpr int kGroup = 16;              // tiles between published entry states
 constexpr int kPolls = 1 << 21;         // about two seconds of polling
-static_assert(kGroup < 32, "one polling lane per tile of a group, one for its entry state");
+static_assert(kGroup <= 32, "one polling lane per tile of a group");
 
 // V channels of one token as they are stored, and as fp32.
 template <typename T, int V> struct Raw;
@@ -95,16 +95,15 @@ template <int V> struct Raw<__nv_bfloat16, V> {
     }
 };
 
-// Workspace of a call with more than one tile: a ticket, a flag per (tile, column)
-// and per (group, column), all zeroed first, then the published (A, B) and entry states.
+// Workspace of a call with more than one tile: a ticket, a flag per (tile, column) and the
+// groups' entry states, all zeroed first, then the published (A, B).
 // A column is one block of 32 V channels of one row of the token axis; tiles and
 // groups are numbered in the order of the scan (from the end in the backward).
 struct ScanWork {
     int* ticket;
     int* tile_flag;    // [tiles][cols]
-    int* group_flag;   // [groups][cols]
+    unsigned long long* entry;   // [groups][cols][32 V]: value, and 1 in the high word once it is there
     float* tile_ab;    // [tiles][cols][2][32 V]
-    float* entry;      // [groups][cols][32 V]
     int64_t cols, tiles;
 };
 
@@ -117,6 +116,27 @@ __device__ __forceinline__ int load_acquire(const int* p)
 __device__ __forceinline__ void store_release(int* p, int v)
 {
     asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long load_relaxed(const unsigned long long* p)
+{
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_relaxed(unsigned long long* p, unsigned long long v)
+{
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+template <int V> __device__ __forceinline__ void load_cg(const float* p, float (&v)[V])
+{
+    if constexpr (V == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = __ldcg(p + e);
+    }
 }
 
 // The state behind a run (A, B) entered with h.  A negative A (-0 too): the run holds the
@@ -206,49 +226,56 @@ __device__ __forceinline__ void tile_carry(const ScanWork& w, int64_t i, int64_t
             __stcg(p + CB + e, B[e]);
         }
         __syncwarp();
-        if (lane == 0) {
-            __threadfence();
-            store_release(w.tile_flag + i * w.cols + col, 1);
+        if (lane == 0) store_release(w.tile_flag + i * w.cols + col, 1);
+    }
+    // the group's earlier tiles as one run: nothing of it waits for the group's entry state
+    float rA[V], rB[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) rA[e] = 1.f, rB[e] = 0.f, carry[e] = 0.f;
+    if (lane < behind) {
+        const int* flag = w.tile_flag + (first + lane) * w.cols + col;
+        for (int k = 0; load_acquire(flag) == 0;)
+            if (++k >= kPolls) {
+                if (err) atomicOr(err, kErrScanWait);
+                break;
+            }
+    }
+    __syncwarp();
+#pragma unroll 8
+    for (int k = 0; k < behind; ++k) {
+        const float* p = w.tile_ab + ((first + k) * w.cols + col) * 2 * CB + lane * V;
+        float pa[V], pb[V];
+        load_cg<V>(p, pa);
+        load_cg<V>(p + CB, pb);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            rB[e] = leave(pa[e], pb[e], rB[e]);
+            rA[e] = chain(rA[e], pa[e]);
         }
     }
+    if (g > 0) {
+        // a published entry state is a word of the value and a tag: it is read as soon as it is there
+        const unsigned long long* p = w.entry + (g * w.cols + col) * CB + lane * V;
+        int k = 0;
 #pragma unroll
-    for (int e = 0; e < V; ++e) carry[e] = 0.f;
-    if (i > 0) {
-        const int* flag = nullptr;
-        if (lane < behind) flag = w.tile_flag + (first + lane) * w.cols + col;
-        else if (lane == 31 && g > 0) flag = w.group_flag + g * w.cols + col;
-        if (flag) {
-            int k = 0;
-            while (load_acquire(flag) == 0)
+        for (int e = 0; e < V; ++e) {
+            unsigned long long v;
+            while (((v = load_relaxed(p + e)) >> 32) == 0)
                 if (++k >= kPolls) {
                     if (err) atomicOr(err, kErrScanWait);
                     break;
                 }
-        }
-        __syncwarp();
-        __threadfence();
-        if (g > 0) {
-            const float* p = w.entry + (g * w.cols + col) * CB + lane * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) carry[e] = __ldcg(p + e);
-        }
-#pragma unroll 4
-        for (int k = 0; k < behind; ++k) {
-            const float* p = w.tile_ab + ((first + k) * w.cols + col) * 2 * CB + lane * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) carry[e] = leave(__ldcg(p + e), __ldcg(p + CB + e), carry[e]);
+            carry[e] = __uint_as_float((unsigned)v);
         }
     }
     if (more && last) {
-        float* p = w.entry + ((g + 1) * w.cols + col) * CB + lane * V;
+        unsigned long long* p = w.entry + ((g + 1) * w.cols + col) * CB + lane * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e) __stcg(p + e, leave(A[e], B[e], carry[e]));
-        __syncwarp();
-        if (lane == 0) {
-            __threadfence();
-            store_release(w.group_flag + (g + 1) * w.cols + col, 1);
-        }
+        for (int e = 0; e < V; ++e)
+            store_relaxed(p + e, (1ull << 32) | __float_as_uint(leave(A[e], B[e], leave(rA[e], rB[e], carry[e]))));
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) carry[e] = leave(rA[e], rB[e], carry[e]);
 }
 
 // (tile in scan order, column) of this CTA: by ticket when tiles wait on one another.
@@ -563,16 +590,15 @@ cudaError_t launch_scan(const GlrArgs& a, bool backward, cudaStream_t st)
     StreamBuffer buf;
     if (w.tiles > 1) {
         const int64_t groups = (w.tiles + kGroup - 1) / kGroup;
-        const int64_t flags = (4 + (w.tiles + groups) * w.cols + 3) / 4 * 4;
-        const int64_t floats = (2 * w.tiles + groups) * w.cols * CB;
-        cudaError_t e = buf.alloc((size_t)(flags + floats) * 4, st);
-        if (e == cudaSuccess) e = cudaMemsetAsync(buf.ptr, 0, (size_t)flags * 4, st);
+        const int64_t flags = (4 + w.tiles * w.cols + 3) / 4 * 4, entries = groups * w.cols * CB;
+        const int64_t zeroed = flags * 4 + entries * 8;
+        cudaError_t e = buf.alloc((size_t)(zeroed + 2 * w.tiles * w.cols * CB * 4), st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(buf.ptr, 0, (size_t)zeroed, st);
         if (e != cudaSuccess) return e;
         w.ticket = static_cast<int*>(buf.ptr);
         w.tile_flag = w.ticket + 4;
-        w.group_flag = w.tile_flag + w.tiles * w.cols;
-        w.tile_ab = reinterpret_cast<float*>(w.ticket + flags);
-        w.entry = w.tile_ab + 2 * w.tiles * w.cols * CB;
+        w.entry = reinterpret_cast<unsigned long long*>(w.ticket + flags);
+        w.tile_ab = reinterpret_cast<float*>(w.entry + entries);
     }
     LaunchScope scope(st, backward ? K_GLR_BWD : K_GLR_FWD);
     const unsigned grid = (unsigned)(w.tiles * w.cols);
