@@ -3,21 +3,31 @@
 // decay), its gradients and its decode step.
 //
 // Scan.  A run of tokens maps the state it enters with affinely, h -> A h + B, and
-// runs compose: the token axis is cut into tiles of kTile tokens, a tile into eight
-// runs of kSteps tokens, one per warp, each lane owning V channels of its run in
-// registers.  One pass over memory:
-//   1. every warp loads its run and folds it into (A, B); the tile's (A, B) is
-//      published in the workspace;
-//   2. the state entering the tile is put together from what earlier tiles
-//      published, in an order that does not depend on timing: the state entering its
-//      group of kGroup tiles, then the (A, B) of the group's earlier tiles one by
-//      one (the last tile of a group publishes the next group's entry state);
-//   3. every warp walks its run again from its entry state and writes the outputs.
-// So a value is the same on every run, and the chain of waits is one hop per
-// kGroup * kTile tokens.  Tiles are taken by a ticket, tokens first: whatever a
-// tile waits for was taken earlier and never waits for it, so every wait ends (and
-// is bounded all the same).  Sequences: a token that begins one replaces the state
-// by h0 (A = 0, B = h0), whatever came before it.
+// runs compose.  A tile is kTile tokens of kCh channels, cut into kRuns runs; the
+// scan is one pass over memory, bound by it, with one persistent CTA per SM whose
+// warps each do one part of the work for the tiles that pass through a ring of
+// shared-memory stages:
+//   loaders      take a tile and start its copies, a few tiles ahead: TMA boxes where
+//                every row starts on 16 bytes, else four more warps copy the 16-byte
+//                chunks that cover each row (cp.async);
+//   aggregators  (two groups of kRuns warps, tiles in turn) fold each run of the
+//                tile into (A, B);
+//   carriers     (three warps, tiles in turn) fold the runs, publish the tile's (A, B)
+//                and put the state that enters the tile together from what earlier
+//                tiles published: the state entering its group of kGroup tiles, then
+//                the (A, B) of the group's earlier tiles, in that order whatever
+//                arrives first; the last tile of a group publishes the state that
+//                enters the next one;
+//   finishers    (two groups of kRuns warps) walk the runs again from their entry
+//                states and write the outputs.
+// So loads, arithmetic and the waits of different tiles overlap, a value is the same on
+// every run, and the chain of waits is one hop per kGroup * kTile tokens.  Tiles are
+// taken by a ticket, first tokens first, and every CTA works through its tiles in
+// that order: whatever a tile waits for was taken earlier and waits for nothing
+// later, so every wait ends (and is bounded all the same).
+//
+// Sequences: a token that begins one replaces the state by h0, whatever came before it
+// (a NaN too): A = -1 there, and a run whose A is negative is h -> B.
 //
 // Backward.  With c_t = exp(log_a_t) g_t, g_t = dout_t + c_{t+1}: the same scan over
 // tiles from the last to the first, replaced by dhT at a sequence's last token.
@@ -26,117 +36,105 @@
 // writes dx, dlog_a once.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_tma.cuh"
+#include "kda_umma.cuh"
 
 namespace kda {
 
 constexpr int kTile = KDA_GLR_TILE;     // tokens of a tile
-constexpr int kWarps = 8;
-constexpr int kSteps = kTile / kWarps;  // tokens of a warp
+constexpr int kCh = 64;                 // channels of a tile, two a lane
+constexpr int kRuns = 4;                // runs of a tile, one a warp
+constexpr int kSteps = kTile / kRuns;   // tokens of a run
 constexpr int kGroup = 16;              // tiles between published entry states
 constexpr int kPolls = 1 << 21;         // about two seconds of polling
-static_assert(kGroup <= 32, "one polling lane per tile of a group");
+constexpr int kScanBit = 7;             // kErrScanWait
+constexpr int kAtOnce = 8;              // published tiles asked for together
 
-// V channels of one token as they are stored, and as fp32.
-template <typename T, int V> struct Raw;
-template <int V> struct Raw<float, V> {
-    float v[V];
-    __device__ __forceinline__ void load(const float* p) {
-        if constexpr (V == 4) {
-            const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        } else if constexpr (V == 2) {
-            const float2 x = __ldcs(reinterpret_cast<const float2*>(p));
-            v[0] = x.x; v[1] = x.y;
-        } else {
-            v[0] = __ldcs(p);
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = 0.f;
-    }
-    __device__ __forceinline__ float get(int e) const { return v[e]; }
-    static __device__ __forceinline__ void store(float* p, const float* v) {
-        if constexpr (V == 4) __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-        else if constexpr (V == 2) __stcs(reinterpret_cast<float2*>(p), make_float2(v[0], v[1]));
-        else __stcs(p, v[0]);
-    }
-};
-template <int V> struct Raw<__nv_bfloat16, V> {
-    uint32_t u[(V + 1) / 2];
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        if constexpr (V == 4) {
-            const uint2 x = __ldcs(reinterpret_cast<const uint2*>(p));
-            u[0] = x.x; u[1] = x.y;
-        } else if constexpr (V == 2) {
-            u[0] = __ldcs(reinterpret_cast<const unsigned int*>(p));
-        } else {
-            u[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int e = 0; e < (V + 1) / 2; ++e) u[e] = 0;
-    }
-    __device__ __forceinline__ float get(int e) const {
-        return __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
-    }
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-        if constexpr (V == 4)
-            __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack(v[0], v[1]), pack(v[2], v[3])));
-        else if constexpr (V == 2)
-            __stcs(reinterpret_cast<unsigned int*>(p), pack(v[0], v[1]));
-        else
-            *p = __float2bfloat16_rn(v[0]);
-    }
-};
+// Warps by role: with TMA 20, five to a quarter of the SM.
+constexpr int kAggWarps = 2 * kRuns, kFinWarps = 2 * kRuns, kCarryWarps = 3, kCopyWarps = 4;
+constexpr int scan_threads(bool aligned) { return 32 * (kAggWarps + kFinWarps + kCarryWarps + 1 + (aligned ? 0 : kCopyWarps)); }
 
-// Workspace of a call with more than one tile: a ticket, a flag per (tile, column) and the
-// groups' entry states, all zeroed first, then the published (A, B).
-// A column is one block of 32 V channels of one row of the token axis; tiles and
-// groups are numbered in the order of the scan (from the end in the backward).
+// Workspace: a ticket, the groups' entry states and the tiles' (A, B), all zeroed by the setup
+// kernel; with cu_seqlens each tile's range of offsets.  A column is one block of kCh
+// channels of one row of the token axis; tiles and groups are numbered in the order of the
+// scan (from the end in the backward).
 struct ScanWork {
-    int* ticket;
-    int* tile_flag;    // [tiles][cols]
-    unsigned long long* entry;   // [groups][cols][32 V]: value, and 1 in the high word once it is there
-    float* tile_ab;    // [tiles][cols][2][32 V]
-    int64_t cols, tiles;
+    int* ticket;                   // null: one tile a column, nothing waits, no ticket needed
+    unsigned long long* entry;     // [groups][cols][kCh]: words (1, state)
+    unsigned long long* tile_ab;   // [tiles][cols][kCh]: words (A, B)
+    int2* range;                   // [tiles]: offsets cu[x .. y - 1] lie in [first token, first + kTile]
+    int64_t cols, tiles, total;    // total = tiles * cols
+    int64_t zeroed;                // 16-byte words from ticket on
 };
 
-__device__ __forceinline__ int load_acquire(const int* p)
+// Published words, two channels at once: A, its lowest bit set as the tag of a word that is there
+// (half a step more on A), and B in the high half.  Each word is read and written whole, so a tag
+// comes with its value and nothing else has to be ordered.
+__device__ __forceinline__ void load_words(const unsigned long long* p, unsigned long long& a, unsigned long long& b)
 {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
 }
-__device__ __forceinline__ void store_release(int* p, int v)
+__device__ __forceinline__ void store_words(unsigned long long* p, const float (&A)[2], const float (&B)[2])
 {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+    const unsigned long long a = ((unsigned long long)__float_as_uint(B[0]) << 32) | __float_as_uint(A[0]) | 1u;
+    const unsigned long long b = ((unsigned long long)__float_as_uint(B[1]) << 32) | __float_as_uint(A[1]) | 1u;
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(a), "l"(b) : "memory");
 }
 
-__device__ __forceinline__ unsigned long long load_relaxed(const unsigned long long* p)
+// 16 bytes global -> shared, the first n of them read and the rest zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n)
 {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// One arrival on `bar` once this thread's copies so far are complete.
+__device__ __forceinline__ void arrive_when_copied(uint64_t* bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
+
+// Two channels at once: a register pair, and one instruction for both.
+struct F2 {
     unsigned long long v;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void store_relaxed(unsigned long long* p, unsigned long long v)
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ float x() const { return __uint_as_float((unsigned)v); }
+    __device__ __forceinline__ float y() const { return __uint_as_float((unsigned)(v >> 32)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
 {
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
 }
-template <int V> __device__ __forceinline__ void load_cg(const float* p, float (&v)[V])
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
 {
-    if constexpr (V == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = __ldcg(p + e);
-    }
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
+// exp of two logarithms of decays: 2^t with t = x / ln 2 rounded, times 1 + r ln 2 for the part r of
+// x / ln 2 that the rounding and the constant dropped, so that large logarithms lose nothing.
+// -200 and below (-inf too) give 0, NaN stays.
+__device__ __forceinline__ F2 decay2(F2 l)
+{
+    float a, b;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(l.x()), "f"(-200.f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(l.y()), "f"(-200.f));
+    constexpr float hi = 1.4426950408889634f, lo = (float)(1.4426950408889634 - (double)hi), ln2 = 0.6931471805599453f;
+    const F2 x(a, b), t = mul2(x, F2(hi, hi));
+    const F2 minus(-t.x(), -t.y());
+    const F2 r = fma2(x, F2(lo, lo), fma2(x, F2(hi, hi), minus));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x()));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y()));
+    const F2 e(a, b);
+    return fma2(mul2(e, F2(ln2, ln2)), r, e);
 }
 
 // The state behind a run (A, B) entered with h.  A negative A (-0 too): the run holds the
@@ -148,11 +146,6 @@ __device__ __forceinline__ float leave(float A, float B, float h)
 // A of a run followed by a run with A = a.
 __device__ __forceinline__ float chain(float A, float a) { return __float_as_int(a) < 0 ? a : A * a; }
 
-// Which sequence begins, and which ends, at each token of a tile (-1: none).
-struct Marks {
-    int first[kTile], last[kTile];
-};
-
 // Row of h0 / hT / the pool that holds sequence n's state; -1: none.
 __device__ __forceinline__ int64_t glr_row(const GlrArgs& a, int64_t n, bool report)
 {
@@ -162,387 +155,599 @@ __device__ __forceinline__ int64_t glr_row(const GlrArgs& a, int64_t n, bool rep
     return s >= 0 && s < a.P ? s : -1;
 }
 
-// Marks of tokens [t0, t0 + kTile) of row b.  All threads call it; the marks are
-// there after the next __syncthreads.  Offsets are found by a search of the whole
-// warp; an array that is not sorted gives some offsets, never an index outside
-// the tile or the arrays.
-__device__ __forceinline__ void find_marks(const GlrArgs& a, int64_t b, int64_t t0, Marks& m)
-{
-    const int tid = threadIdx.x;
-    if (a.cu == nullptr) {
-        if (tid < kTile) {
-            m.first[tid] = t0 + tid == 0 ? (int)b : -1;
-            m.last[tid] = t0 + tid == a.T - 1 ? (int)b : -1;
-        }
-        return;
+// Rows of a tile in shared memory.  Aligned: every row of the tensor starts on 16 bytes and
+// holds whole 16-byte chunks, lane l owns channels 2 l, 2 l + 1.  Otherwise the chunks that
+// cover a row are copied, one more than its bytes need, the row starts (row index * D) mod
+// (16 bytes) elements into them, and lane l owns channels l, l + 32.
+template <typename E, bool Aligned>
+struct Rows {
+    static constexpr int kBytes = kCh * (int)sizeof(E);
+    static constexpr int kPitch = kBytes + (Aligned ? 0 : 16);
+    static constexpr int kPer16 = 16 / (int)sizeof(E);
+
+    // Copies of rows [r0, r1) of the tile, whose row 0 is row `first`; rows from `live` on read as
+    // zeros; channels from c0.  Unaligned rows only.
+    static __device__ __forceinline__ void copy(unsigned char* dst, const E* src, int64_t first, int r0, int r1,
+                                                int live, int64_t D, int64_t c0, int64_t total)
+    {
+        constexpr int kChunks = kBytes / 16, kRowsAtOnce = 32 / kChunks;
+        const int lane = threadIdx.x % 32;
+        strip(umma::smem_u32(dst), src, first, r0 + lane / kChunks, r1, live, D, c0, total, kRowsAtOnce, lane % kChunks);
+        strip(umma::smem_u32(dst), src, first, r0 + lane, r1, live, D, c0, total, 32, kChunks);
     }
-    if (tid < kTile) m.first[tid] = m.last[tid] = -1;
-    __syncthreads();
-    if (tid >= 32) return;
-    int64_t lo = 0, hi = a.N + 1;                // first index with cu[index] >= t0 lies in [lo, hi]
-    while (hi - lo > 32) {
-        const int64_t step = (hi - lo + 31) / 32, i = lo + tid * step;
-        const int c = __popc(__ballot_sync(0xffffffffu, i < hi && a.cu[i] < t0));
-        if (c == 0) {
-            hi = lo;
+    // One chunk of rows r0, r0 + step, ..
+    static __device__ __forceinline__ void strip(uint32_t to, const E* src, int64_t first, int r0, int r1, int live,
+                                                 int64_t D, int64_t c0, int64_t total, const int step, int chunk)
+    {
+        const unsigned char* at = reinterpret_cast<const unsigned char*>(src + (first + r0) * D + c0);
+        const unsigned char* end = reinterpret_cast<const unsigned char*>(src + total);
+        const int64_t pitch = step * D * (int64_t)sizeof(E);
+        const int left = (int)((D - c0 < kCh ? D - c0 : kCh) * sizeof(E)) - chunk * 16;    // row bytes from the chunk on
+        to += r0 * kPitch + chunk * 16;
+#pragma unroll 4
+        for (int r = r0; r < r1; r += step, at += pitch, to += step * kPitch) {
+            const int into = (int)(reinterpret_cast<uintptr_t>(at) & 15);
+            const unsigned char* p = at - into + chunk * 16;
+            const bool in = r < live && left + into > 0;
+            const int64_t rest = end - p;        // never past the tensor's end
+            copy16(to, in ? p : reinterpret_cast<const unsigned char*>(src), in ? rest < 16 ? (int)rest : 16 : 0);
+        }
+    }
+    // Elements into its chunks at which row `row` starts.
+    static __device__ __forceinline__ int shift(int64_t row, int64_t D)
+    {
+        return Aligned ? 0 : (int)((row * D) % kPer16);
+    }
+    // The lane's two channels of row r of the tile.
+    static __device__ __forceinline__ F2 get(const unsigned char* base, int r, int shift, int lane)
+    {
+        const E* p = reinterpret_cast<const E*>(base + r * kPitch);
+        if constexpr (!Aligned) return F2(IO<E>::load(p, shift + lane), IO<E>::load(p, shift + lane + 32));
+        if constexpr (sizeof(E) == 4) {
+            F2 v;
+            v.v = reinterpret_cast<const unsigned long long*>(p)[lane];
+            return v;
         } else {
-            lo += (c - 1) * step + 1;
-            hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+            const uint32_t u = reinterpret_cast<const uint32_t*>(p)[lane];
+            return F2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
         }
     }
-    lo += __popc(__ballot_sync(0xffffffffu, lo + tid < hi && a.cu[lo + tid] < t0));
-    for (int64_t base = lo; base <= a.N; base += 32) {
-        const int64_t i = base + tid;
-        const int64_t o = i <= a.N ? a.cu[i] - t0 : kTile + 1;
-        if (o >= 0 && o < kTile && i < a.N && a.cu[i + 1] > a.cu[i]) m.first[o] = (int)i;
-        if (o > 0 && o <= kTile && i > 0 && a.cu[i - 1] < a.cu[i]) m.last[o - 1] = (int)(i - 1);
-        if (__any_sync(0xffffffffu, o > kTile)) break;
+    static __device__ __forceinline__ void put(unsigned char* base, int r, int shift, int lane, F2 v)
+    {
+        static_assert(sizeof(E) == 4, "decays only");
+        float* p = reinterpret_cast<float*>(base + r * kPitch);
+        if constexpr (Aligned) {
+            reinterpret_cast<unsigned long long*>(p)[lane] = v.v;
+        } else {
+            p[shift + lane] = v.x();
+            p[shift + lane + 32] = v.y();
+        }
+    }
+};
+
+// The lane's two channels, from c0, of a row of a tensor in global memory; on0, on1: which of
+// them exist (aligned: both or none).
+template <typename E, bool Aligned>
+__device__ __forceinline__ void store_pair(E* at, bool on0, bool on1, F2 v)
+{
+    if constexpr (Aligned) {
+        if (!on0) return;
+        if constexpr (sizeof(E) == 4) {
+            __stcs(reinterpret_cast<float2*>(at), make_float2(v.x(), v.y()));
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x(), v.y());
+            __stcs(reinterpret_cast<unsigned int*>(at), *reinterpret_cast<const unsigned int*>(&h));
+        }
+    } else {
+        if (on0) IO<E>::store(at, 0, v.x());
+        if (on1) IO<E>::store(at, 32, v.y());
+    }
+}
+template <bool Aligned>
+__device__ __forceinline__ F2 load_pair(const float* at, bool on0, bool on1)
+{
+    return F2(at && on0 ? at[0] : 0.f, at && on1 ? at[Aligned ? 1 : 32] : 0.f);
+}
+
+// One stage of the ring.
+template <typename T, bool Aligned, bool Bwd>
+struct Stage {
+    using La = Rows<float, Aligned>;
+    using X = Rows<T, Aligned>;
+    alignas(128) unsigned char la[kTile * La::kPitch];           // log_a, then exp(log_a)
+    alignas(128) unsigned char x[kTile * X::kPitch];
+    alignas(128) unsigned char y[Bwd ? kTile * X::kPitch : 128]; // dout
+    float A[kRuns][kCh], B[kRuns][kCh];                          // runs in the scan's direction
+    float fA[Bwd ? kRuns : 1][kCh], fB[Bwd ? kRuns : 1][kCh];    // backward: the forward runs too
+    float carry[kCh];
+    int first[kTile], last[kTile];                               // sequences that begin / end there, or -1
+    int64_t id;                                                  // tile * cols + column; -1: no more
+    int marked;                                                  // whether first / last hold anything
+    uint64_t taken, full, agg, carried, empty;
+    static constexpr uint32_t kCopied = kTile * (La::kBytes + X::kBytes * (Bwd ? 2 : 1));
+};
+template <typename T, bool Aligned, bool Bwd> constexpr int ring_stages()
+{
+    constexpr int n = (int)((227 * 1024 - 64) / sizeof(Stage<T, Aligned, Bwd>));
+    return n < 8 ? n : 8;
+}
+
+// Where a tile lies (tiles, columns and their product fit 31 bits).
+struct TileAt {
+    uint32_t order, col, i;                      // order: in the scan; i: on the token axis
+    int64_t b, t0, row0, c0;                     // row0 = b * T + t0
+    __device__ __forceinline__ TileAt(const GlrArgs& a, const ScanWork& w, int64_t id, bool bwd)
+    {
+        order = (uint32_t)id / (uint32_t)w.cols;
+        col = (uint32_t)id - order * (uint32_t)w.cols;
+        i = bwd ? (uint32_t)w.tiles - 1 - order : order;
+        const uint32_t blocks = (uint32_t)((a.D + kCh - 1) / kCh), row = col / blocks;
+        b = row;
+        c0 = (int64_t)(col - row * blocks) * kCh;
+        t0 = (int64_t)i * kTile;
+        row0 = b * a.T + t0;
+    }
+};
+
+// Before a scan: zeroes the ticket, flags and entry states, finds every tile's offsets, checks
+// the offsets, and passes the states of sequences without tokens on.
+__global__ void __launch_bounds__(256) glr_setup_kernel(GlrArgs a, ScanWork w, int bwd)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t me = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
+    for (int64_t k = me; k < w.zeroed; k += all) reinterpret_cast<uint4*>(w.ticket)[k] = make_uint4(0, 0, 0, 0);
+    if (a.cu) {
+        for (int64_t i = me; i < w.tiles; i += all) {
+            int at[2];
+            for (int k = 0; k < 2; ++k) {
+                const int64_t bound = i * kTile + (k ? kTile + 1 : 0);
+                int64_t lo = 0, hi = a.N + 1;    // first index with cu[index] >= bound
+                while (lo < hi) {
+                    const int64_t mid = (lo + hi) >> 1;
+                    if (a.cu[mid] < bound) lo = mid + 1; else hi = mid;
+                }
+                at[k] = (int)lo;
+            }
+            w.range[i] = make_int2(at[0], at[1]);
+        }
+        for (int64_t n = me; n < a.N; n += all)
+            if (a.cu[n + 1] < a.cu[n] || (n == 0 && (a.cu[0] != 0 || a.cu[a.N] != a.T))) atomicOr(a.err, kErrSeqlens);
+    }
+    const float* from = bwd ? a.dhT : a.h0;
+    float* to = bwd ? a.dh0 : a.hT;
+    if ((!a.cu && a.T > 0) || to == nullptr) return;
+    for (int64_t n = me / 32; n < a.N; n += all / 32) {
+        if (a.cu && a.cu[n + 1] > a.cu[n]) continue;
+        const int64_t row = bwd ? n : glr_row(a, n, me % 32 == 0);
+        if (row < 0 || to == from) continue;
+        for (int64_t c = me % 32; c < a.D; c += 32) to[row * a.D + c] = from ? from[row * a.D + c] : 0.f;
     }
 }
 
-// Offsets that are not sorted from 0 to T; each tile looks at its share.
-__device__ __forceinline__ void check_offsets(const GlrArgs& a, int64_t tile, int64_t tiles)
-{
-    for (int64_t n = tile * blockDim.x + threadIdx.x; n < a.N; n += tiles * blockDim.x)
-        if (a.cu[n + 1] < a.cu[n] || (n == 0 && (a.cu[0] != 0 || a.cu[a.N] != a.T))) atomicOr(a.err, kErrSeqlens);
-}
+// Tensor maps of log_a, x and dout (aligned rows).
+struct ScanMaps {
+    CUtensorMap la, x, y;
+};
 
-// The state entering tile i of column col: every lane its V channels, in `carry`.  One warp.
-// ab: the tile's own (A, B), published for the tiles behind it.
-template <int V>
-__device__ __forceinline__ void tile_carry(const ScanWork& w, int64_t i, int64_t col, const float (&A)[V],
-                                           const float (&B)[V], float (&carry)[V], int* err)
+// The loader warp that takes the tiles, marks their sequences and, for aligned rows, starts the
+// copies.
+template <typename T, bool Aligned, bool Bwd, int NS>
+__device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, const ScanMaps& maps,
+                                          Stage<T, Aligned, Bwd>* ring)
 {
-    constexpr int CB = 32 * V;
+    using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32;
-    const int64_t g = i / kGroup, first = g * kGroup;
-    const int behind = (int)(i - first);         // earlier tiles of the group
-    const bool last = behind == kGroup - 1, more = i + 1 < w.tiles;
-    if (more && !last) {
-        float* p = w.tile_ab + (i * w.cols + col) * 2 * CB + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            __stcg(p + e, A[e]);
-            __stcg(p + CB + e, B[e]);
+    int64_t next = blockIdx.x;
+    if (w.ticket) {
+        int v = 0;
+        if (lane == 0) v = atomicAdd(w.ticket, 1);
+        next = __shfl_sync(0xffffffffu, v, 0);
+    }
+    int ends = 0;
+    for (int64_t q = 0; ends < kCarryWarps; ++q) {
+        S& s = ring[q % NS];
+        const int64_t id = next < w.total ? next : -1;
+        int v = 0;
+        if (w.ticket && id >= 0 && lane == 0) v = atomicAdd(w.ticket, 1);   // the next tile's, on its way meanwhile
+        const TileAt at(a, w, id < 0 ? 0 : id, Bwd);
+        int2 range = make_int2(0, 0);
+        if (a.cu && id >= 0) range = w.range[at.i];
+        if (q >= NS && !umma::mbar_wait(&s.empty, (uint32_t)((q / NS - 1) & 1), a.err, kScanBit)) {
+            // given up: the copies under way have to land before the CTA may end
+            for (int64_t k = q - NS; k < q; ++k)
+                umma::mbar_wait(&ring[k % NS].full, (uint32_t)((k / NS) & 1), a.err, kScanBit);
+            return;
+        }
+        if (id < 0) ++ends;                      // one for every worker that takes tiles in turn
+        if (lane == 0) {
+            s.id = id;
+            if constexpr (Aligned) {
+                if (id >= 0) {
+                    tma::expect_tx(&s.full, S::kCopied);
+                    tma::load_3d(s.la, &maps.la, (int)at.c0, (int)at.t0, (int)at.b, &s.full);
+                    tma::load_3d(s.x, &maps.x, (int)at.c0, (int)at.t0, (int)at.b, &s.full);
+                    if constexpr (Bwd) tma::load_3d(s.y, &maps.y, (int)at.c0, (int)at.t0, (int)at.b, &s.full);
+                } else {
+                    umma::mbar_arrive(&s.full);
+                }
+            } else {
+                umma::mbar_arrive(&s.taken);
+            }
+        }
+        if (id >= 0) {
+            // sequences that begin or end in the tile
+            const bool begins = !a.cu && at.t0 == 0, ends_here = !a.cu && at.t0 + kTile >= a.T;
+            const bool marked = a.cu ? range.y > range.x : begins || ends_here;
+            if (lane == 0) s.marked = marked;
+            if (marked) {
+                for (int t = lane; t < kTile; t += 32) {
+                    s.first[t] = begins && t == 0 ? (int)at.b : -1;
+                    s.last[t] = ends_here && at.t0 + t == a.T - 1 ? (int)at.b : -1;
+                }
+                __syncwarp();
+                for (int64_t k = range.x + lane; k < range.y; k += 32) {
+                    const int64_t o = a.cu[k] - at.t0;
+                    if (o >= 0 && o < kTile && k < a.N && a.cu[k + 1] > a.cu[k]) s.first[o] = (int)k;
+                    if (o > 0 && o <= kTile && k > 0 && a.cu[k - 1] < a.cu[k]) s.last[o - 1] = (int)(k - 1);
+                }
+            }
         }
         __syncwarp();
-        if (lane == 0) store_release(w.tile_flag + i * w.cols + col, 1);
+        if (lane == 0) umma::mbar_arrive(&s.full);
+        if (w.ticket) next = __shfl_sync(0xffffffffu, v, 0);
+        else next += gridDim.x;
+        if (id < 0) next = w.total;
     }
-    // the group's earlier tiles as one run: nothing of it waits for the group's entry state
-    float rA[V], rB[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) rA[e] = 1.f, rB[e] = 0.f, carry[e] = 0.f;
-    if (lane < behind) {
-        const int* flag = w.tile_flag + (first + lane) * w.cols + col;
-        for (int k = 0; load_acquire(flag) == 0;)
-            if (++k >= kPolls) {
-                if (err) atomicOr(err, kErrScanWait);
-                break;
-            }
-    }
-    __syncwarp();
-#pragma unroll 8
-    for (int k = 0; k < behind; ++k) {
-        const float* p = w.tile_ab + ((first + k) * w.cols + col) * 2 * CB + lane * V;
-        float pa[V], pb[V];
-        load_cg<V>(p, pa);
-        load_cg<V>(p + CB, pb);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            rB[e] = leave(pa[e], pb[e], rB[e]);
-            rA[e] = chain(rA[e], pa[e]);
+}
+
+// A copying warp (unaligned rows): its share of every tile's rows.
+template <typename T, bool Bwd, int NS>
+__device__ __forceinline__ void scan_copy(const GlrArgs& a, const ScanWork& w, Stage<T, false, Bwd>* ring, int share)
+{
+    using S = Stage<T, false, Bwd>;
+    const int64_t total = a.B * a.T * a.D;
+    const int r0 = share * (kTile / kCopyWarps), r1 = r0 + kTile / kCopyWarps;
+    int ends = 0;
+    for (int64_t q = 0; ends < kCarryWarps; ++q) {
+        S& s = ring[q % NS];
+        if (!umma::mbar_wait(&s.taken, (uint32_t)((q / NS) & 1), a.err, kScanBit)) break;
+        if (s.id < 0) {
+            ++ends;
+        } else {
+            const TileAt at(a, w, s.id, Bwd);
+            const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile);
+            S::La::copy(s.la, a.log_a, at.row0, r0, r1, live, a.D, at.c0, total);
+            S::X::copy(s.x, (const T*)a.x, at.row0, r0, r1, live, a.D, at.c0, total);
+            if constexpr (Bwd) S::X::copy(s.y, (const T*)a.dout, at.row0, r0, r1, live, a.D, at.c0, total);
         }
+        arrive_when_copied(&s.full);
     }
-    if (g > 0) {
-        // a published entry state is a word of the value and a tag: it is read as soon as it is there
-        const unsigned long long* p = w.entry + (g * w.cols + col) * CB + lane * V;
-        int k = 0;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// An aggregator warp: run `run` of every second tile, from tile `group` on.
+template <typename T, bool Aligned, bool Bwd, int NS>
+__device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring,
+                                               int group, int run)
+{
+    using S = Stage<T, Aligned, Bwd>;
+    const int lane = threadIdx.x % 32, r0 = run * kSteps;
+    const int dl = (int)(a.D % S::La::kPer16), dx = (int)(a.D % S::X::kPer16);   // shifts from row to row
+    for (int64_t q = group;; q += 2) {
+        S& s = ring[q % NS];
+        if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
+        const TileAt at(a, w, s.id, Bwd);
+        int sl = S::La::shift(at.row0 + r0, a.D), sx = S::X::shift(at.row0 + r0, a.D);
+        F2 A(1.f, 1.f), B(0.f, 0.f);
+        if (!s.marked) {
+#pragma unroll 4
+            for (int k = 0; k < kSteps; ++k) {
+                const F2 l = decay2(S::La::get(s.la, r0 + k, sl, lane));
+                A = mul2(A, l);
+                B = fma2(l, B, S::X::get(s.x, r0 + k, sx, lane));
+                S::La::put(s.la, r0 + k, sl, lane, l);   // the finishers take the decay from here
+                sl = (sl + dl) % S::La::kPer16;
+                sx = (sx + dx) % S::X::kPer16;
+            }
+            if constexpr (Bwd) {
+                *reinterpret_cast<F2*>(&s.fA[run][2 * lane]) = A;
+                *reinterpret_cast<F2*>(&s.fB[run][2 * lane]) = B;
+                // the product of the decays is the same from either end but for its rounding
+                B = F2(0.f, 0.f);
+#pragma unroll 4
+                for (int k = kSteps - 1; k >= 0; --k) {
+                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
+                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
+                    B = mul2(S::La::get(s.la, r0 + k, sl, lane), add2(B, S::X::get(s.y, r0 + k, sx, lane)));
+                }
+            }
+        } else {
+            const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
+            const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
+            for (int k = 0; k < kSteps; ++k) {
+                const int r = r0 + k;
+                F2 l = decay2(S::La::get(s.la, r, sl, lane));
+                const F2 x = S::X::get(s.x, r, sx, lane);
+                const int n = s.first[r];
+                if (n >= 0) {
+                    const int64_t row = Bwd ? n : glr_row(a, n, lane == 0 && at.c0 == 0);
+                    const F2 h0 = load_pair<Aligned>(a.h0 && row >= 0 ? a.h0 + row * a.D + c : nullptr, on0, on1);
+                    A = F2(-1.f, -1.f);
+                    B = add2(mul2(l, h0), x);
+                    if constexpr (!Bwd) {
+                        // the finishers find exp(log_a) h0 here: hT may be written over h0 before they come
+                        l = mul2(l, h0);
+                        if (a.starts && r == 0)
+                            store_pair<float, Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, h0);
+                    }
+                } else {
+                    A = mul2(A, l);
+                    B = fma2(l, B, x);
+                }
+                S::La::put(s.la, r, sl, lane, l);
+                sl = (sl + dl) % S::La::kPer16;
+                sx = (sx + dx) % S::X::kPer16;
+            }
+            if constexpr (Bwd) {
+                *reinterpret_cast<F2*>(&s.fA[run][2 * lane]) = A;
+                *reinterpret_cast<F2*>(&s.fB[run][2 * lane]) = B;
+                A = F2(1.f, 1.f);
+                B = F2(0.f, 0.f);
+                for (int k = kSteps - 1; k >= 0; --k) {
+                    const int r = r0 + k;
+                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
+                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
+                    const int n = s.last[r];
+                    if (n >= 0) {
+                        A = F2(-1.f, -1.f);
+                        B = load_pair<Aligned>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
+                    }
+                    const F2 l = S::La::get(s.la, r, sl, lane);
+                    A = mul2(A, l);
+                    B = mul2(l, add2(B, S::X::get(s.y, r, sx, lane)));
+                }
+            }
+        }
+        *reinterpret_cast<F2*>(&s.A[run][2 * lane]) = A;
+        *reinterpret_cast<F2*>(&s.B[run][2 * lane]) = B;
+        // the decays written over log_a come before the TMA copy that fills the stage again
+        if constexpr (Aligned) umma::fence_smem_to_async();
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&s.agg);
+    }
+}
+
+// A carrier warp: every third tile, from tile `first` on.
+template <typename T, bool Aligned, bool Bwd, int NS>
+__device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring, int from)
+{
+    using S = Stage<T, Aligned, Bwd>;
+    const int lane = threadIdx.x % 32;
+    for (int64_t q = from;; q += kCarryWarps) {
+        S& s = ring[q % NS];
+        // the end is announced by the loader alone
+        if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
+        if (!umma::mbar_wait(&s.agg, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
+        const TileAt at(a, w, s.id, Bwd);
+        const int64_t g = at.order / kGroup, first = g * kGroup;
+        const int behind = (int)(at.order - first);      // earlier tiles of the group
+        const bool last = behind == kGroup - 1, more = at.order + 1 < w.tiles;
+        float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            unsigned long long v;
-            while (((v = load_relaxed(p + e)) >> 32) == 0)
-                if (++k >= kPolls) {
-                    if (err) atomicOr(err, kErrScanWait);
+        for (int k = 0; k < kRuns; ++k) {
+            const int run = Bwd ? kRuns - 1 - k : k;
+            const float2 ra = *reinterpret_cast<const float2*>(&s.A[run][2 * lane]);
+            const float2 rb = *reinterpret_cast<const float2*>(&s.B[run][2 * lane]);
+            B[0] = leave(ra.x, rb.x, B[0]);
+            B[1] = leave(ra.y, rb.y, B[1]);
+            A[0] = chain(A[0], ra.x);
+            A[1] = chain(A[1], ra.y);
+        }
+        if (more && !last) store_words(w.tile_ab + ((int64_t)at.order * w.cols + at.col) * kCh + 2 * lane, A, B);
+        // an entry state is a word of the value and a tag: it is read as soon as it is there, and
+        // asked for now
+        const unsigned long long* entry = w.entry + (g * w.cols + at.col) * kCh + 2 * lane;
+        unsigned long long e0 = 0, e1 = 0;
+        if (g > 0) load_words(entry, e0, e1);
+        // the group's earlier tiles as one run: nothing of it waits for the group's entry state
+        float rA[2] = {1.f, 1.f}, rB[2] = {0.f, 0.f}, carry[2] = {0.f, 0.f};
+        const unsigned long long* ab = w.tile_ab + (first * w.cols + at.col) * kCh + 2 * lane;
+        int polls = 0;
+        for (int k0 = 0; k0 < behind; k0 += kAtOnce) {
+            unsigned long long v0[kAtOnce], v1[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (k0 + k < behind) load_words(ab + (int64_t)(k0 + k) * w.cols * kCh, v0[k], v1[k]);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (k0 + k < behind) {
+                    while (!(v0[k] & v1[k] & 1)) {
+                        if (++polls >= kPolls) {
+                            if (a.err) atomicOr(a.err, kErrScanWait);
+                            break;
+                        }
+                        load_words(ab + (int64_t)(k0 + k) * w.cols * kCh, v0[k], v1[k]);
+                    }
+                    const float pa[2] = {__uint_as_float((unsigned)v0[k]), __uint_as_float((unsigned)v1[k])};
+                    rB[0] = leave(pa[0], __uint_as_float((unsigned)(v0[k] >> 32)), rB[0]);
+                    rB[1] = leave(pa[1], __uint_as_float((unsigned)(v1[k] >> 32)), rB[1]);
+                    rA[0] = chain(rA[0], pa[0]);
+                    rA[1] = chain(rA[1], pa[1]);
+                }
+        }
+        if (g > 0) {
+            while (!(e0 & e1 & 1)) {
+                if (++polls >= kPolls) {
+                    if (a.err) atomicOr(a.err, kErrScanWait);
                     break;
                 }
-            carry[e] = __uint_as_float((unsigned)v);
+                load_words(entry, e0, e1);
+            }
+            carry[0] = __uint_as_float((unsigned)(e0 >> 32));
+            carry[1] = __uint_as_float((unsigned)(e1 >> 32));
         }
+        carry[0] = leave(rA[0], rB[0], carry[0]);
+        carry[1] = leave(rA[1], rB[1], carry[1]);
+        if (more && last) {
+            const float one[2] = {1.f, 1.f}, out[2] = {leave(A[0], B[0], carry[0]), leave(A[1], B[1], carry[1])};
+            store_words(w.entry + ((g + 1) * w.cols + at.col) * kCh + 2 * lane, one, out);
+        }
+        *reinterpret_cast<float2*>(&s.carry[2 * lane]) = make_float2(carry[0], carry[1]);
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&s.carried);
     }
-    if (more && last) {
-        unsigned long long* p = w.entry + ((g + 1) * w.cols + col) * CB + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            store_relaxed(p + e, (1ull << 32) | __float_as_uint(leave(A[e], B[e], leave(rA[e], rB[e], carry[e]))));
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) carry[e] = leave(rA[e], rB[e], carry[e]);
 }
 
-// (tile in scan order, column) of this CTA: by ticket when tiles wait on one another.
-__device__ __forceinline__ int64_t take_tile(const ScanWork& w, int& slot)
+// A finisher warp: run `run` of every second tile, from tile `group` on.
+template <typename T, bool Aligned, bool Bwd, int NS>
+__device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring,
+                                            int group, int run)
 {
-    if (w.tiles == 1) return blockIdx.x;
-    if (threadIdx.x == 0) slot = atomicAdd(w.ticket, 1);
-    __syncthreads();
-    return slot;
-}
-
-template <typename T, int V>
-__global__ void __launch_bounds__(kWarps * 32, 3) glr_fwd_kernel(GlrArgs a, ScanWork w)
-{
-    constexpr int CB = 32 * V;
-    __shared__ float sA[kWarps][CB], sB[kWarps][CB], sC[CB];
-    __shared__ Marks marks;
-    __shared__ int slot;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t id = take_tile(w, slot);
-    const int64_t i = id / w.cols, col = id - i * w.cols;
-    const int64_t blocks = (a.D + CB - 1) / CB, b = col / blocks;
-    const int64_t c = (col - b * blocks) * CB + lane * V;
-    const bool on = c < a.D;
-    const int64_t t0 = i * kTile, tw = t0 + warp * kSteps;
-    const int64_t at = (b * a.T + tw) * a.D + c;
-
-    Raw<T, V> x[kSteps];
-    Raw<float, V> al[kSteps];
+    using S = Stage<T, Aligned, Bwd>;
+    const int lane = threadIdx.x % 32, r0 = run * kSteps;
+    const int dl = (int)(a.D % S::La::kPer16), dx = (int)(a.D % S::X::kPer16);
+    for (int64_t q = group;; q += 2) {
+        S& s = ring[q % NS];
+        if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
+        const TileAt at(a, w, s.id, Bwd);
+        const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile) - r0;   // tokens of the run that exist
+        const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
+        const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
+        F2 enter(0.f, 0.f);                      // backward: the kept entry state, asked for before the wait
+        if constexpr (Bwd) enter = load_pair<Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1);
+        if (!umma::mbar_wait(&s.carried, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
+        const bool plain = !s.marked && live >= kSteps;
+        int sl = S::La::shift(at.row0 + r0, a.D), sx = S::X::shift(at.row0 + r0, a.D);
+        float h[2];
+        if constexpr (!Bwd) {
+            h[0] = s.carry[2 * lane];
+            h[1] = s.carry[2 * lane + 1];
+            for (int k = 0; k < run; ++k)
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        if (on && tw + s < a.T) {
-            al[s].load(a.log_a + at + s * a.D);
-            x[s].load((const T*)a.x + at + s * a.D);
-        } else {                                  // past the end: h stays as it is
-            al[s].clear();
-            x[s].clear();
-        }
-    }
-    find_marks(a, b, t0, marks);
-    __syncthreads();
-    if (a.cu && col == 0) check_offsets(a, i, w.tiles);
-
-    float A[V], B[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) A[e] = 1.f, B[e] = 0.f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) al[s].v[e] = expf(al[s].v[e]);
-        const int n = marks.first[warp * kSteps + s];
-        if (n >= 0) {
-            // from here on this token's register holds exp(log_a) h0: hT may be written over h0
-            // before the second walk
-            const int64_t row = glr_row(a, n, lane == 0 && c == 0);
-            const bool has = a.h0 && row >= 0 && on;
-            float h0[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) h0[e] = has ? a.h0[row * a.D + c + e] : 0.f;
-            if (a.starts && warp == 0 && s == 0 && on)
-                Raw<float, V>::store(a.starts + (b * w.tiles + i) * a.D + c, h0);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                al[s].v[e] *= h0[e];
-                A[e] = -1.f;
-                B[e] = al[s].v[e] + x[s].get(e);
+                for (int e = 0; e < 2; ++e) h[e] = leave(s.A[k][2 * lane + e], s.B[k][2 * lane + e], h[e]);
+            F2 H(h[0], h[1]);
+            if (a.starts && run == 0 && live > 0 && !(s.marked && s.first[0] >= 0))
+                store_pair<float, Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, H);
+            T* out = (T*)a.out + (at.row0 + r0) * a.D + c;
+            if (plain && a.out) {
+#pragma unroll 4
+                for (int k = 0; k < kSteps; ++k, out += a.D) {
+                    H = fma2(S::La::get(s.la, r0 + k, sl, lane), H, S::X::get(s.x, r0 + k, sx, lane));
+                    store_pair<T, Aligned>(out, on0, on1, H);
+                    sl = (sl + dl) % S::La::kPer16;
+                    sx = (sx + dx) % S::X::kPer16;
+                }
+            } else {
+                for (int k = 0; k < live && k < kSteps; ++k, out += a.D) {
+                    const int r = r0 + k;
+                    const F2 l = S::La::get(s.la, r, sl, lane), x = S::X::get(s.x, r, sx, lane);
+                    H = s.marked && s.first[r] >= 0 ? add2(l, x) : fma2(l, H, x);
+                    if (a.out) store_pair<T, Aligned>(out, on0, on1, H);
+                    const int n = s.marked && a.hT ? s.last[r] : -1;
+                    if (n >= 0) {
+                        const int64_t row = glr_row(a, n, false);
+                        if (row >= 0) store_pair<float, Aligned>(a.hT + row * a.D + c, on0, on1, H);
+                    }
+                    sl = (sl + dl) % S::La::kPer16;
+                    sx = (sx + dx) % S::X::kPer16;
+                }
             }
         } else {
+            // the state before every token of the run
+            F2 before[kSteps];
+            h[0] = enter.x();
+            h[1] = enter.y();
+            float g[2] = {s.carry[2 * lane], s.carry[2 * lane + 1]};     // c of the token behind
+            for (int k = 0; k < run; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                A[e] *= al[s].v[e];
-                B[e] = al[s].v[e] * B[e] + x[s].get(e);
+                for (int e = 0; e < 2; ++e) h[e] = leave(s.fA[k][2 * lane + e], s.fB[k][2 * lane + e], h[e]);
+            for (int k = kRuns - 1; k > run; --k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) g[e] = leave(s.A[k][2 * lane + e], s.B[k][2 * lane + e], g[e]);
+            F2 H(h[0], h[1]), G(g[0], g[1]);
+            if (plain) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    before[k] = H;
+                    H = fma2(S::La::get(s.la, r0 + k, sl, lane), H, S::X::get(s.x, r0 + k, sx, lane));
+                    sl = (sl + dl) % S::La::kPer16;
+                    sx = (sx + dx) % S::X::kPer16;
+                }
+                T* to = (T*)a.dx + (at.row0 + r0 + kSteps - 1) * a.D + c;
+                float* ta = a.dlog_a + (at.row0 + r0 + kSteps - 1) * a.D + c;
+#pragma unroll
+                for (int k = kSteps - 1; k >= 0; --k, to -= a.D, ta -= a.D) {
+                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
+                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
+                    G = add2(G, S::X::get(s.y, r0 + k, sx, lane));
+                    store_pair<T, Aligned>(to, on0, on1, G);
+                    G = mul2(G, S::La::get(s.la, r0 + k, sl, lane));
+                    store_pair<float, Aligned>(ta, on0, on1, mul2(G, before[k]));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const int n = s.marked ? s.first[r0 + k] : -1;
+                    if (n >= 0)
+                        H = load_pair<Aligned>(a.h0 ? a.h0 + (int64_t)n * a.D + c : nullptr, on0, on1);
+                    before[k] = H;
+                    H = fma2(S::La::get(s.la, r0 + k, sl, lane), H, S::X::get(s.x, r0 + k, sx, lane));
+                    sl = (sl + dl) % S::La::kPer16;
+                    sx = (sx + dx) % S::X::kPer16;
+                }
+#pragma unroll
+                for (int k = kSteps - 1; k >= 0; --k) {
+                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
+                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
+                    if (k >= live) continue;
+                    const int n = s.marked ? s.last[r0 + k] : -1;
+                    if (n >= 0)
+                        G = load_pair<Aligned>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
+                    G = add2(G, S::X::get(s.y, r0 + k, sx, lane));
+                    const int64_t to = (at.row0 + r0 + k) * a.D + c;
+                    store_pair<T, Aligned>((T*)a.dx + to, on0, on1, G);
+                    G = mul2(G, S::La::get(s.la, r0 + k, sl, lane));
+                    store_pair<float, Aligned>(a.dlog_a + to, on0, on1, mul2(G, before[k]));
+                    const int m = s.marked && a.dh0 ? s.first[r0 + k] : -1;
+                    if (m >= 0) store_pair<float, Aligned>(a.dh0 + (int64_t)m * a.D + c, on0, on1, G);
+                }
             }
         }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&s.empty);
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sA[warp][lane * V + e] = A[e], sB[warp][lane * V + e] = B[e];
-    __syncthreads();
-    if (warp == 0) {
-        float carry[V];
-#pragma unroll
-        for (int k = 1; k < kWarps; ++k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float ak = sA[k][lane * V + e];
-                B[e] = leave(ak, sB[k][lane * V + e], B[e]);
-                A[e] = chain(A[e], ak);
-            }
-        tile_carry<V>(w, i, col, A, B, carry, a.err);
-#pragma unroll
-        for (int e = 0; e < V; ++e) sC[lane * V + e] = carry[e];
-    }
-    __syncthreads();
-    float h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = sC[lane * V + e];
-    for (int k = 0; k < warp; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = leave(sA[k][lane * V + e], sB[k][lane * V + e], h[e]);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int64_t t = tw + s;
-        if (t >= a.T) break;
-        const bool begins = marks.first[warp * kSteps + s] >= 0;
-        if (a.starts && warp == 0 && s == 0 && on && !begins)
-            Raw<float, V>::store(a.starts + (b * w.tiles + i) * a.D + c, h);
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = (begins ? al[s].v[e] : al[s].v[e] * h[e]) + x[s].get(e);
-        if (a.out && on) Raw<T, V>::store((T*)a.out + at + s * a.D, h);
-        const int m = marks.last[warp * kSteps + s];
-        if (m >= 0 && a.hT) {
-            const int64_t row = glr_row(a, m, false);
-            if (row >= 0 && on) Raw<float, V>::store(a.hT + row * a.D + c, h);
-        }
-    }
-    // sequences without tokens: every tile takes its share, a warp a sequence
-    if ((a.cu || a.T == 0) && a.hT)
-        for (int64_t n = i * kWarps + warp; n < a.N; n += w.tiles * kWarps)
-            if (!a.cu || a.cu[n + 1] <= a.cu[n]) {
-                const int64_t row = glr_row(a, n, lane == 0 && c == 0);
-                if (row >= 0 && on)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) a.hT[row * a.D + c + e] = a.h0 ? a.h0[row * a.D + c + e] : 0.f;
-            }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(GlrArgs a, ScanWork w)
+template <typename T, bool Aligned, bool Bwd>
+__global__ void __launch_bounds__(scan_threads(Aligned), 1)
+glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
 {
-    constexpr int CB = 32 * V;
-    __shared__ float sA[kWarps][CB], sB[kWarps][CB], sC[CB];     // backward runs
-    __shared__ float fA[kWarps][CB], fB[kWarps][CB];             // forward runs
-    __shared__ Marks marks;
-    __shared__ int slot;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t id = take_tile(w, slot);
-    const int64_t order = id / w.cols, col = id - order * w.cols;
-    const int64_t i = w.tiles - 1 - order;       // the last tile first
-    const int64_t blocks = (a.D + CB - 1) / CB, b = col / blocks;
-    const int64_t c = (col - b * blocks) * CB + lane * V;
-    const bool on = c < a.D;
-    const int64_t t0 = i * kTile, tw = t0 + warp * kSteps;
-    const int64_t at = (b * a.T + tw) * a.D + c;
-
-    Raw<T, V> x[kSteps], y[kSteps];
-    Raw<float, V> al[kSteps];
-    Raw<float, V> enter;
-    enter.clear();
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        if (on && tw + s < a.T) {
-            al[s].load(a.log_a + at + s * a.D);
-            x[s].load((const T*)a.x + at + s * a.D);
-            y[s].load((const T*)a.dout + at + s * a.D);
-        } else {
-            al[s].clear();
-            x[s].clear();
-            y[s].clear();
-        }
-    }
-    if (on && a.T > 0) enter.load(a.starts + (b * w.tiles + i) * a.D + c);
-    find_marks(a, b, t0, marks);
-    __syncthreads();
-    if (a.cu && col == 0) check_offsets(a, i, w.tiles);
-
-    float A[V], B[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) A[e] = 1.f, B[e] = 0.f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int n = marks.first[warp * kSteps + s];
-        if (n >= 0)
-#pragma unroll
-            for (int e = 0; e < V; ++e) A[e] = -1.f, B[e] = a.h0 && on ? a.h0[n * a.D + c + e] : 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            al[s].v[e] = expf(al[s].v[e]);
-            A[e] *= al[s].v[e];
-            B[e] = al[s].v[e] * B[e] + x[s].get(e);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) fA[warp][lane * V + e] = A[e], fB[warp][lane * V + e] = B[e];
-#pragma unroll
-    for (int e = 0; e < V; ++e) A[e] = 1.f, B[e] = 0.f;
-#pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s) {
-        const int n = marks.last[warp * kSteps + s];
-        if (n >= 0)
-#pragma unroll
-            for (int e = 0; e < V; ++e) A[e] = -1.f, B[e] = a.dhT && on ? a.dhT[n * a.D + c + e] : 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            A[e] *= al[s].v[e];
-            B[e] = al[s].v[e] * (B[e] + y[s].get(e));
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sA[warp][lane * V + e] = A[e], sB[warp][lane * V + e] = B[e];
-    __syncthreads();
-    if (warp == kWarps - 1) {
-        float carry[V];
-#pragma unroll
-        for (int k = kWarps - 2; k >= 0; --k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float ak = sA[k][lane * V + e];
-                B[e] = leave(ak, sB[k][lane * V + e], B[e]);
-                A[e] = chain(A[e], ak);
-            }
-        tile_carry<V>(w, order, col, A, B, carry, a.err);
-#pragma unroll
-        for (int e = 0; e < V; ++e) sC[lane * V + e] = carry[e];
-    }
-    // states before every token of the run, while the carry is on its way
-    float h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = enter.v[e];
-    for (int k = 0; k < warp; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = leave(fA[k][lane * V + e], fB[k][lane * V + e], h[e]);
-    float before[kSteps][V];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int n = marks.first[warp * kSteps + s];
-        if (n >= 0)
-#pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = a.h0 && on ? a.h0[n * a.D + c + e] : 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            before[s][e] = h[e];
-            h[e] = al[s].v[e] * h[e] + x[s].get(e);
-        }
+    griddep_wait();
+    using S = Stage<T, Aligned, Bwd>;
+    constexpr int NS = ring_stages<T, Aligned, Bwd>();
+    static_assert(NS > kCarryWarps, "the ends take a stage each");
+    extern __shared__ __align__(128) unsigned char smem[];
+    S* ring = reinterpret_cast<S*>(smem);
+    int warp = threadIdx.x / 32;
+    if (threadIdx.x < NS) {
+        S& s = ring[threadIdx.x];
+        umma::mbar_init(&s.taken, 1);
+        umma::mbar_init(&s.full, Aligned ? 2 : 1 + 32 * kCopyWarps);   // the marks, and the copies
+        umma::mbar_init(&s.agg, kRuns);
+        umma::mbar_init(&s.carried, 1);
+        umma::mbar_init(&s.empty, kRuns);
+        umma::fence_mbar_init();
     }
     __syncthreads();
-    float g[V];                                   // c of the token behind
-#pragma unroll
-    for (int e = 0; e < V; ++e) g[e] = sC[lane * V + e];
-    for (int k = kWarps - 1; k > warp; --k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = leave(sA[k][lane * V + e], sB[k][lane * V + e], g[e]);
-#pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s) {
-        const int64_t t = tw + s;
-        if (t >= a.T) continue;
-        const int n = marks.last[warp * kSteps + s];
-        if (n >= 0)
-#pragma unroll
-            for (int e = 0; e < V; ++e) g[e] = a.dhT && on ? a.dhT[n * a.D + c + e] : 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) g[e] += y[s].get(e);
-        if (on) Raw<T, V>::store((T*)a.dx + at + s * a.D, g);
-        float dl[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            g[e] *= al[s].v[e];
-            dl[e] = g[e] * before[s][e];
-        }
-        if (on) Raw<float, V>::store(a.dlog_a + at + s * a.D, dl);
-        const int m = marks.first[warp * kSteps + s];
-        if (m >= 0 && a.dh0 && on) Raw<float, V>::store(a.dh0 + (int64_t)m * a.D + c, g);
-    }
-    if ((a.cu || a.T == 0) && a.dh0)
-        for (int64_t n = i * kWarps + warp; n < a.N; n += w.tiles * kWarps)
-            if ((!a.cu || a.cu[n + 1] <= a.cu[n]) && on)
-#pragma unroll
-                for (int e = 0; e < V; ++e) a.dh0[n * a.D + c + e] = a.dhT ? a.dhT[n * a.D + c + e] : 0.f;
+    if (warp < kAggWarps) return scan_aggregate<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
+    warp -= kAggWarps;
+    if (warp < kFinWarps) return scan_finish<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
+    warp -= kFinWarps;
+    if (warp < kCarryWarps) return scan_carry<T, Aligned, Bwd, NS>(a, w, ring, warp);
+    warp -= kCarryWarps;
+    if (warp == 0) return scan_load<T, Aligned, Bwd, NS>(a, w, maps, ring);
+    if constexpr (!Aligned) scan_copy<T, Bwd, NS>(a, w, ring, warp - 1);
 }
 
 template <typename T>
@@ -570,64 +775,63 @@ glr_step_kernel(const T* __restrict__ x, const float* __restrict__ log_a, float*
 
 namespace {
 
-// V channels a lane: the widest access that D allows, halved while it would leave half of
-// the lanes without channels.
-int lane_channels(int64_t D)
+template <typename T, bool Aligned, bool Bwd>
+cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
 {
-    int v = D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;
-    while (v > 1 && 16 * v >= D) v /= 2;
-    return v;
-}
-
-template <typename T, int V>
-cudaError_t launch_scan(const GlrArgs& a, bool backward, cudaStream_t st)
-{
-    constexpr int64_t CB = 32 * V;
     ScanWork w = {};
-    w.cols = a.B * ((a.D + CB - 1) / CB);
-    w.tiles = a.T > 0 ? (a.T + kTile - 1) / kTile : 1;
-    if (w.tiles > 0x7fffffffLL / w.cols) return cudaErrorInvalidConfiguration;
+    w.cols = a.B * ((a.D + kCh - 1) / kCh);
+    w.tiles = (a.T + kTile - 1) / kTile;
+    w.total = w.tiles * w.cols;
     StreamBuffer buf;
-    if (w.tiles > 1) {
+    // a single tile per column waits for nothing: no ticket, no setup, unless offsets or
+    // sequences without tokens want looking at
+    if (w.tiles > 1 || a.cu || a.T == 0) {
         const int64_t groups = (w.tiles + kGroup - 1) / kGroup;
-        const int64_t flags = (4 + w.tiles * w.cols + 3) / 4 * 4, entries = groups * w.cols * CB;
-        const int64_t zeroed = flags * 4 + entries * 8;
-        cudaError_t e = buf.alloc((size_t)(zeroed + 2 * w.tiles * w.cols * CB * 4), st);
-        if (e == cudaSuccess) e = cudaMemsetAsync(buf.ptr, 0, (size_t)zeroed, st);
+        const int64_t words = (groups * w.cols + w.total) * kCh, ranges = (w.tiles + 1) / 2 * 2;
+        const cudaError_t e = buf.alloc((size_t)(16 + (words + ranges) * 8), st);
         if (e != cudaSuccess) return e;
         w.ticket = static_cast<int*>(buf.ptr);
-        w.tile_flag = w.ticket + 4;
-        w.entry = reinterpret_cast<unsigned long long*>(w.ticket + flags);
-        w.tile_ab = reinterpret_cast<float*>(w.entry + entries);
+        w.entry = reinterpret_cast<unsigned long long*>(w.ticket + 4);
+        w.tile_ab = w.entry + groups * w.cols * kCh;
+        w.range = reinterpret_cast<int2*>(w.tile_ab + w.total * kCh);
+        w.zeroed = 1 + words / 2;
+        const int64_t work = w.zeroed / 8 + (a.cu ? w.tiles : 0) + (a.cu || a.T == 0 ? a.N * 32 : 0);
+        const int64_t ctas = (work + 255) / 256;
+        LaunchScope scope(st, K_GLR_SETUP);
+        const cudaError_t s = launch_pdl(glr_setup_kernel, dim3((unsigned)(ctas < 296 ? ctas < 1 ? 1 : ctas : 296)),
+                                         dim3(256), 0, st, a, w, Bwd ? 1 : 0);
+        if (s != cudaSuccess) return s;
     }
-    LaunchScope scope(st, backward ? K_GLR_BWD : K_GLR_FWD);
-    const unsigned grid = (unsigned)(w.tiles * w.cols);
-    if (backward) glr_bwd_kernel<T, V><<<grid, kWarps * 32, 0, st>>>(a, w);
-    else glr_fwd_kernel<T, V><<<grid, kWarps * 32, 0, st>>>(a, w);
-    return cudaGetLastError();
+    if (w.total == 0) return cudaSuccess;
+    constexpr int smem = ring_stages<T, Aligned, Bwd>() * (int)sizeof(Stage<T, Aligned, Bwd>);
+    const auto kernel = glr_scan_kernel<T, Aligned, Bwd>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ScanMaps maps = {};
+    if (Aligned) {
+        constexpr bool bf16 = sizeof(T) == 2;
+        cudaError_t m = make_tensor_map_3d(&maps.la, a.log_a, false, a.D, a.T, a.B, kCh, kTile);
+        if (m == cudaSuccess) m = make_tensor_map_3d(&maps.x, a.x, bf16, a.D, a.T, a.B, kCh, kTile);
+        if (m == cudaSuccess && Bwd) m = make_tensor_map_3d(&maps.y, a.dout, bf16, a.D, a.T, a.B, kCh, kTile);
+        if (m != cudaSuccess) return m;
+    }
+    LaunchScope scope(st, Bwd ? K_GLR_BWD : K_GLR_FWD);
+    return launch_pdl(kernel, dim3((unsigned)(w.total < kSMs ? w.total : kSMs)), dim3(scan_threads(Aligned)), smem, st,
+                      a, w, maps);
 }
 
-template <typename T>
-cudaError_t launch_scan_t(const GlrArgs& a, bool backward, cudaStream_t st)
+template <bool Bwd>
+cudaError_t launch_scan_t(const GlrArgs& a, cudaStream_t st)
 {
-    switch (lane_channels(a.D)) {
-    case 4: return launch_scan<T, 4>(a, backward, st);
-    case 2: return launch_scan<T, 2>(a, backward, st);
-    }
-    return launch_scan<T, 1>(a, backward, st);
+    if (a.io == KDA_IO_F32)
+        return a.D % 4 == 0 ? launch_scan<float, true, Bwd>(a, st) : launch_scan<float, false, Bwd>(a, st);
+    return a.D % 8 == 0 ? launch_scan<__nv_bfloat16, true, Bwd>(a, st) : launch_scan<__nv_bfloat16, false, Bwd>(a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st)
-{
-    return a.io == KDA_IO_F32 ? launch_scan_t<float>(a, false, st) : launch_scan_t<__nv_bfloat16>(a, false, st);
-}
-
-cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st)
-{
-    return a.io == KDA_IO_F32 ? launch_scan_t<float>(a, true, st) : launch_scan_t<__nv_bfloat16>(a, true, st);
-}
+cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st) { return launch_scan_t<false>(a, st); }
+cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st) { return launch_scan_t<true>(a, st); }
 
 cudaError_t launch_glr_step(const void* x, const float* log_a, float* state, const int32_t* slots,
                             void* out, int64_t N, int64_t P, int64_t D, kda_io_dtype_t io, int* err,
@@ -653,12 +857,16 @@ namespace {
 constexpr int64_t kMaxChannels = int64_t(1) << 20;
 constexpr int64_t kMaxTokens = int64_t(1) << 40;
 
-kda_status_t glr_check_sizes(int64_t B, int64_t T, int64_t D, kda_io_dtype_t io)
+// Rows, channels and tokens; `rows` = 1 with cu_seqlens.
+kda_status_t glr_check_sizes(int64_t B, int64_t T, int64_t D, kda_io_dtype_t io, bool packed)
 {
     if (B < 0 || T < 0 || D < 0) return KDA_ERR_INVALID_ARG;
     if (io != KDA_IO_F32 && io != KDA_IO_BF16) return KDA_ERR_UNSUPPORTED;
-    if (D > kMaxChannels || B > 0x7fffffffLL || T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
-    if (B > 0 && T > kMaxTokens / B) return KDA_ERR_UNSUPPORTED;
+    if (D > kMaxChannels || B > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (T > 0x7fffffffLL || (B > 0 && T > kMaxTokens / B)) return KDA_ERR_UNSUPPORTED;
+    // tickets and offsets are 32-bit
+    const int64_t cols = (packed ? 1 : B) * ((D + kCh - 1) / kCh);
+    if (cols > 0 && (T + kTile - 1) / kTile > (0x7fffffffLL - 65536) / cols) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -666,7 +874,7 @@ kda_status_t glr_fwd_impl(const void* x, const float* log_a, const float* h0, vo
                           float* starts, const int32_t* slots, int64_t P, const int32_t* cu,
                           int64_t B, int64_t T, int64_t D, kda_io_dtype_t io, cudaStream_t stream)
 {
-    const kda_status_t s = glr_check_sizes(B, T, D, io);
+    const kda_status_t s = glr_check_sizes(B, T, D, io, cu != nullptr);
     if (s != KDA_OK) return s;
     if (cu && B < 1) return KDA_ERR_INVALID_ARG;
     if (B == 0 || D == 0) return KDA_OK;
@@ -741,7 +949,7 @@ kda_status_t kda_glr_scan_bwd(const void* x, const float* log_a, const float* h0
                               float* dlog_a, float* dh0, const int32_t* cu_seqlens, int64_t B,
                               int64_t T, int64_t D, kda_io_dtype_t io_dtype, cudaStream_t stream)
 {
-    const kda_status_t s = glr_check_sizes(B, T, D, io_dtype);
+    const kda_status_t s = glr_check_sizes(B, T, D, io_dtype, cu_seqlens != nullptr);
     if (s != KDA_OK) return s;
     if (cu_seqlens && B < 1) return KDA_ERR_INVALID_ARG;
     if (B == 0 || D == 0) return KDA_OK;

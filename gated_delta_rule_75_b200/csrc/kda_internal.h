@@ -251,6 +251,7 @@ enum KernelId {
     K_BWD_DENSE2,
     K_BWD_PARAM,
     K_FUSED_TC,
+    K_GLR_SETUP,
     K_GLR_FWD,
     K_GLR_BWD,
     K_GLR_STEP,
@@ -393,6 +394,7 @@ struct GlrArgs {
     kda_io_dtype_t io;
     int* err;
 };
+constexpr int kSMs = 148;     // of a B200: CTAs of a persistent grid
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st);
 cudaError_t launch_glr_step(const void* x, const float* log_a, float* state, const int32_t* slots,

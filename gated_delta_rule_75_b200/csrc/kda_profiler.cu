@@ -17,7 +17,7 @@ static const char* const kKernelNames[K_KERNEL_COUNT] = {
     "chunk_offsets", "chunk_prep_simt", "chunk_state_simt", "decode_step",
     "chunk_prep_tc", "chunk_state_tc", "chunk_state_seg_tc", "affine_prefix", "fill",
     "bwd_state", "bwd_dense1", "bwd_dense2", "bwd_param", "chunk_fused_tc",
-    "glr_scan_fwd", "glr_scan_bwd", "glr_step", "tree_fwd", "tree_commit",
+    "glr_setup", "glr_scan_fwd", "glr_scan_bwd", "glr_step", "tree_fwd", "tree_commit",
     "group_norm_fwd", "group_norm_bwd", "group_norm_wgrad",
 };
 
