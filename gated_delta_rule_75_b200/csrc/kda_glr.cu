@@ -7,24 +7,31 @@
 // scan is one pass over memory, bound by it, with one persistent CTA per SM whose
 // warps each do one part of the work for the tiles that pass through a ring of
 // shared-memory stages:
-//   loaders      take a tile and start its copies, a few tiles ahead: TMA boxes where
-//                every row starts on 16 bytes, else four more warps copy the 16-byte
-//                chunks that cover each row (cp.async);
+//   loader       takes tiles and starts their TMA copies, a few tiles ahead;
 //   aggregators  (two groups of kRuns warps, tiles in turn) fold each run of the
-//                tile into (A, B);
-//   carriers     (three warps, tiles in turn) fold the runs, publish the tile's (A, B)
-//                and put the state that enters the tile together from what earlier
-//                tiles published: the state entering its group of kGroup tiles, then
-//                the (A, B) of the group's earlier tiles, in that order whatever
-//                arrives first; the last tile of a group publishes the state that
-//                enters the next one;
+//                tile into (A, B), and the runs into the tile's, and publish that;
+//   carriers     (a warp per stage but one, tiles in turn) put the state that enters the
+//                tile together, from when the tile is taken, of what earlier
+//                tiles published: the state entering its group of kBlocks blocks of
+//                kBlock tiles, then the (A, B) of the group's earlier blocks, then
+//                those of the block's earlier tiles, in that order whatever arrives
+//                first; the last tile of a block publishes the block's (A, B), or,
+//                in the last block, the state that enters the next group;
 //   finishers    (two groups of kRuns warps) walk the runs again from their entry
 //                states and write the outputs.
 // So loads, arithmetic and the waits of different tiles overlap, a value is the same on
-// every run, and the chain of waits is one hop per kGroup * kTile tokens.  Tiles are
-// taken by a ticket, first tokens first, and every CTA works through its tiles in
-// that order: whatever a tile waits for was taken earlier and waits for nothing
-// later, so every wait ends (and is bounded all the same).
+// every run, and the chain of waits is one hop per group.  CTA c takes tiles c, c + grid, ..
+// (first tokens first; all CTAs are resident, by a cooperative launch) and works through
+// them in that order: whatever a tile waits for comes before it in some CTA's order and
+// waits for nothing later, so every wait ends (and is bounded all the same).  Handing tiles
+// out by a counter instead lets a tile be taken long before it is loaded, and those
+// behind it wait for it.
+//
+// Rows that do not start on 16 bytes.  TMA wants strides of 16 bytes: R = 2, 4 or 8 rows
+// together have one, and the tensor is read as rows of R D elements.  A tile is then R
+// boxes, one for each place of a token in such a row, that start on the 16-byte boundary
+// before its channels and are 16 bytes wider.  The last tokens of the tensor, fewer than R,
+// are read by the workers themselves.
 //
 // Sequences: a token that begins one replaces the state by h0, whatever came before it
 // (a NaN too): A = -1 there, and a run whose A is negative is h -> B.
@@ -45,26 +52,46 @@ constexpr int kTile = KDA_GLR_TILE;     // tokens of a tile
 constexpr int kCh = 64;                 // channels of a tile, two a lane
 constexpr int kRuns = 4;                // runs of a tile, one a warp
 constexpr int kSteps = kTile / kRuns;   // tokens of a run
-constexpr int kGroup = 16;              // tiles between published entry states
+constexpr int kBlock = 8;               // tiles of a block
+constexpr int kBlocks = 8;              // blocks of a group
 constexpr int kPolls = 1 << 21;         // about two seconds of polling
 constexpr int kScanBit = 7;             // kErrScanWait
-constexpr int kAtOnce = 8;              // published tiles asked for together
 
-// Warps by role: with TMA 20, five to a quarter of the SM.
-constexpr int kAggWarps = 2 * kRuns, kFinWarps = 2 * kRuns, kCarryWarps = 3, kCopyWarps = 4;
-constexpr int scan_threads(bool aligned) { return 32 * (kAggWarps + kFinWarps + kCarryWarps + 1 + (aligned ? 0 : kCopyWarps)); }
+// Warps by role.
+constexpr int kAggWarps = 2 * kRuns, kFinWarps = 2 * kRuns;
+constexpr int carry_warps(int stages) { return stages - 1; }
+constexpr int scan_threads(int stages) { return 32 * (kAggWarps + kFinWarps + carry_warps(stages) + 1); }
 
-// Workspace: a ticket, the groups' entry states and the tiles' (A, B), all zeroed by the setup
+// n / d for 0 <= n < 2^31 as (n m) >> s: with 2^k >= d, s = 31 + k and m = ceil(2^s / d), n m / 2^s
+// exceeds n / d by less than n / 2^s 2^-0 <= 2^-k <= 1 / d, which reaches no further integer.
+struct Divide {
+    uint32_t m, s;
+    Divide() = default;
+    explicit Divide(int64_t d)
+    {
+        uint32_t k = 0;
+        while ((int64_t(1) << k) < d) ++k;
+        s = 31 + k;
+        m = (uint32_t)(((uint64_t(1) << s) + (uint64_t)d - 1) / (uint64_t)d);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> s); }
+};
+
+// Workspace: the groups' entry states and the blocks' and tiles' (A, B), all zeroed by the setup
 // kernel; with cu_seqlens each tile's range of offsets.  A column is one block of kCh
-// channels of one row of the token axis; tiles and groups are numbered in the order of the
-// scan (from the end in the backward).
+// channels of one row of the token axis; tiles, blocks and groups are numbered in the order of
+// the scan (from the end in the backward).
 struct ScanWork {
-    int* ticket;                   // null: one tile a column, nothing waits, no ticket needed
     unsigned long long* entry;     // [groups][cols][kCh]: words (1, state)
+    unsigned long long* block_ab;  // [blocks][cols][kCh]: words (A, B)
     unsigned long long* tile_ab;   // [tiles][cols][kCh]: words (A, B)
     int2* range;                   // [tiles]: offsets cu[x .. y - 1] lie in [first token, first + kTile]
     int64_t cols, tiles, total;    // total = tiles * cols
-    int64_t zeroed;                // 16-byte words from ticket on
+    Divide by_cols, by_blocks;     // by cols, and by the columns of one row
+    int64_t zeroed;                // 16-byte words from entry on
+    uint32_t blocks;               // columns of one row
+    int log_r;                     // R = 1 << log_r rows of the tensor are one row of the tensor maps
+    int64_t mapped;                // tokens (over all rows) that the tensor maps cover
 };
 
 // Published words, two channels at once: A, its lowest bit set as the tag of a word that is there
@@ -79,17 +106,6 @@ __device__ __forceinline__ void store_words(unsigned long long* p, const float (
     const unsigned long long a = ((unsigned long long)__float_as_uint(B[0]) << 32) | __float_as_uint(A[0]) | 1u;
     const unsigned long long b = ((unsigned long long)__float_as_uint(B[1]) << 32) | __float_as_uint(A[1]) | 1u;
     asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(a), "l"(b) : "memory");
-}
-
-// 16 bytes global -> shared, the first n of them read and the rest zero.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-// One arrival on `bar` once this thread's copies so far are complete.
-__device__ __forceinline__ void arrive_when_copied(uint64_t* bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
 
 // Two channels at once: a register pair, and one instruction for both.
@@ -155,54 +171,20 @@ __device__ __forceinline__ int64_t glr_row(const GlrArgs& a, int64_t n, bool rep
     return s >= 0 && s < a.P ? s : -1;
 }
 
-// Rows of a tile in shared memory.  Aligned: every row of the tensor starts on 16 bytes and
-// holds whole 16-byte chunks, lane l owns channels 2 l, 2 l + 1.  Otherwise the chunks that
-// cover a row are copied, one more than its bytes need, the row starts (row index * D) mod
-// (16 bytes) elements into them, and lane l owns channels l, l + 32.
+// A tile in shared memory.  Aligned rows: kTile rows of kCh elements, lane l owns channels 2 l,
+// 2 l + 1.  Otherwise R boxes of kTile / R rows; lane l owns channels l, l + 32, and the offset
+// of a token's channel 0 is looked up (Stage::off).
 template <typename E, bool Aligned>
 struct Rows {
     static constexpr int kBytes = kCh * (int)sizeof(E);
     static constexpr int kPitch = kBytes + (Aligned ? 0 : 16);
     static constexpr int kPer16 = 16 / (int)sizeof(E);
 
-    // Copies of rows [r0, r1) of the tile, whose row 0 is row `first`; rows from `live` on read as
-    // zeros; channels from c0.  Unaligned rows only.
-    static __device__ __forceinline__ void copy(unsigned char* dst, const E* src, int64_t first, int r0, int r1,
-                                                int live, int64_t D, int64_t c0, int64_t total)
+    // The lane's two channels of the row at `at` bytes.
+    static __device__ __forceinline__ F2 get(const unsigned char* base, int at, int lane)
     {
-        constexpr int kChunks = kBytes / 16, kRowsAtOnce = 32 / kChunks;
-        const int lane = threadIdx.x % 32;
-        strip(umma::smem_u32(dst), src, first, r0 + lane / kChunks, r1, live, D, c0, total, kRowsAtOnce, lane % kChunks);
-        strip(umma::smem_u32(dst), src, first, r0 + lane, r1, live, D, c0, total, 32, kChunks);
-    }
-    // One chunk of rows r0, r0 + step, ..
-    static __device__ __forceinline__ void strip(uint32_t to, const E* src, int64_t first, int r0, int r1, int live,
-                                                 int64_t D, int64_t c0, int64_t total, const int step, int chunk)
-    {
-        const unsigned char* at = reinterpret_cast<const unsigned char*>(src + (first + r0) * D + c0);
-        const unsigned char* end = reinterpret_cast<const unsigned char*>(src + total);
-        const int64_t pitch = step * D * (int64_t)sizeof(E);
-        const int left = (int)((D - c0 < kCh ? D - c0 : kCh) * sizeof(E)) - chunk * 16;    // row bytes from the chunk on
-        to += r0 * kPitch + chunk * 16;
-#pragma unroll 4
-        for (int r = r0; r < r1; r += step, at += pitch, to += step * kPitch) {
-            const int into = (int)(reinterpret_cast<uintptr_t>(at) & 15);
-            const unsigned char* p = at - into + chunk * 16;
-            const bool in = r < live && left + into > 0;
-            const int64_t rest = end - p;        // never past the tensor's end
-            copy16(to, in ? p : reinterpret_cast<const unsigned char*>(src), in ? rest < 16 ? (int)rest : 16 : 0);
-        }
-    }
-    // Elements into its chunks at which row `row` starts.
-    static __device__ __forceinline__ int shift(int64_t row, int64_t D)
-    {
-        return Aligned ? 0 : (int)((row * D) % kPer16);
-    }
-    // The lane's two channels of row r of the tile.
-    static __device__ __forceinline__ F2 get(const unsigned char* base, int r, int shift, int lane)
-    {
-        const E* p = reinterpret_cast<const E*>(base + r * kPitch);
-        if constexpr (!Aligned) return F2(IO<E>::load(p, shift + lane), IO<E>::load(p, shift + lane + 32));
+        const E* p = reinterpret_cast<const E*>(base + at);
+        if constexpr (!Aligned) return F2(IO<E>::load(p, lane), IO<E>::load(p, lane + 32));
         if constexpr (sizeof(E) == 4) {
             F2 v;
             v.v = reinterpret_cast<const unsigned long long*>(p)[lane];
@@ -212,16 +194,21 @@ struct Rows {
             return F2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
         }
     }
-    static __device__ __forceinline__ void put(unsigned char* base, int r, int shift, int lane, F2 v)
+    static __device__ __forceinline__ void put(unsigned char* base, int at, int lane, F2 v)
     {
         static_assert(sizeof(E) == 4, "decays only");
-        float* p = reinterpret_cast<float*>(base + r * kPitch);
+        float* p = reinterpret_cast<float*>(base + at);
         if constexpr (Aligned) {
             reinterpret_cast<unsigned long long*>(p)[lane] = v.v;
         } else {
-            p[shift + lane] = v.x();
-            p[shift + lane + 32] = v.y();
+            p[lane] = v.x();
+            p[lane + 32] = v.y();
         }
+    }
+    // The same from the tensor itself.
+    static __device__ __forceinline__ F2 direct(const E* at, bool on0, bool on1)
+    {
+        return F2(on0 ? IO<E>::load(at, 0) : 0.f, on1 ? IO<E>::load(at, Aligned ? 1 : 32) : 0.f);
     }
 };
 
@@ -259,12 +246,17 @@ struct Stage {
     alignas(128) unsigned char y[Bwd ? kTile * X::kPitch : 128]; // dout
     float A[kRuns][kCh], B[kRuns][kCh];                          // runs in the scan's direction
     float fA[Bwd ? kRuns : 1][kCh], fB[Bwd ? kRuns : 1][kCh];    // backward: the forward runs too
-    float carry[kCh];
+    float tA[kCh], tB[kCh], carry[kCh];                          // the tile; what enters it
     int first[kTile], last[kTile];                               // sequences that begin / end there, or -1
+    int off[Aligned ? 1 : kTile];                                // bytes of a token's channel 0: la | x << 16
     int64_t id;                                                  // tile * cols + column; -1: no more
     int marked;                                                  // whether first / last hold anything
-    uint64_t taken, full, agg, carried, empty;
-    static constexpr uint32_t kCopied = kTile * (La::kBytes + X::kBytes * (Bwd ? 2 : 1));
+    int plain;                                                   // no marks, all tokens there and in the maps
+    uint64_t taken, full, runs, agg, carried, empty;
+    static constexpr uint32_t kCopied = kTile * (La::kPitch + X::kPitch * (Bwd ? 2 : 1));
+
+    __device__ __forceinline__ int la_at(int r) const { return Aligned ? r * La::kPitch : off[r] & 0xffff; }
+    __device__ __forceinline__ int x_at(int r) const { return Aligned ? r * X::kPitch : (int)((uint32_t)off[r] >> 16); }
 };
 template <typename T, bool Aligned, bool Bwd> constexpr int ring_stages()
 {
@@ -278,26 +270,34 @@ struct TileAt {
     int64_t b, t0, row0, c0;                     // row0 = b * T + t0
     __device__ __forceinline__ TileAt(const GlrArgs& a, const ScanWork& w, int64_t id, bool bwd)
     {
-        order = (uint32_t)id / (uint32_t)w.cols;
+        order = w.by_cols((uint32_t)id);
         col = (uint32_t)id - order * (uint32_t)w.cols;
         i = bwd ? (uint32_t)w.tiles - 1 - order : order;
-        const uint32_t blocks = (uint32_t)((a.D + kCh - 1) / kCh), row = col / blocks;
+        const uint32_t row = w.by_blocks(col);
         b = row;
-        c0 = (int64_t)(col - row * blocks) * kCh;
+        c0 = (int64_t)(col - row * w.blocks) * kCh;
         t0 = (int64_t)i * kTile;
         row0 = b * a.T + t0;
     }
 };
 
-// Before a scan: zeroes the ticket, flags and entry states, finds every tile's offsets, checks
+// Before a scan: zeroes the published words, finds every tile's offsets, checks
 // the offsets, and passes the states of sequences without tokens on.
 __global__ void __launch_bounds__(256) glr_setup_kernel(GlrArgs a, ScanWork w, int bwd)
 {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t me = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
-    for (int64_t k = me; k < w.zeroed; k += all) reinterpret_cast<uint4*>(w.ticket)[k] = make_uint4(0, 0, 0, 0);
+    for (int64_t k = me; k < w.zeroed; k += all) reinterpret_cast<uint4*>(w.entry)[k] = make_uint4(0, 0, 0, 0);
     if (a.cu) {
+        // few offsets are searched in shared memory: one trip to memory, not one per step
+        constexpr int kHeld = 4096;
+        __shared__ int32_t held[kHeld];
+        const bool hold = a.N < kHeld;
+        if (hold)
+            for (int64_t n = threadIdx.x; n <= a.N; n += 256) held[n] = a.cu[n];
+        __syncthreads();
+        const int32_t* cu = hold ? held : a.cu;
         for (int64_t i = me; i < w.tiles; i += all) {
             int at[2];
             for (int k = 0; k < 2; ++k) {
@@ -305,14 +305,14 @@ __global__ void __launch_bounds__(256) glr_setup_kernel(GlrArgs a, ScanWork w, i
                 int64_t lo = 0, hi = a.N + 1;    // first index with cu[index] >= bound
                 while (lo < hi) {
                     const int64_t mid = (lo + hi) >> 1;
-                    if (a.cu[mid] < bound) lo = mid + 1; else hi = mid;
+                    if (cu[mid] < bound) lo = mid + 1; else hi = mid;
                 }
                 at[k] = (int)lo;
             }
             w.range[i] = make_int2(at[0], at[1]);
         }
         for (int64_t n = me; n < a.N; n += all)
-            if (a.cu[n + 1] < a.cu[n] || (n == 0 && (a.cu[0] != 0 || a.cu[a.N] != a.T))) atomicOr(a.err, kErrSeqlens);
+            if (cu[n + 1] < cu[n] || (n == 0 && (cu[0] != 0 || cu[a.N] != a.T))) atomicOr(a.err, kErrSeqlens);
     }
     const float* from = bwd ? a.dhT : a.h0;
     float* to = bwd ? a.dh0 : a.hT;
@@ -330,26 +330,19 @@ struct ScanMaps {
     CUtensorMap la, x, y;
 };
 
-// The loader warp that takes the tiles, marks their sequences and, for aligned rows, starts the
-// copies.
+// The loader: one warp.
 template <typename T, bool Aligned, bool Bwd, int NS>
 __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, const ScanMaps& maps,
                                           Stage<T, Aligned, Bwd>* ring)
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32;
+    const int R = Aligned ? 1 : 1 << w.log_r;
     int64_t next = blockIdx.x;
-    if (w.ticket) {
-        int v = 0;
-        if (lane == 0) v = atomicAdd(w.ticket, 1);
-        next = __shfl_sync(0xffffffffu, v, 0);
-    }
     int ends = 0;
-    for (int64_t q = 0; ends < kCarryWarps; ++q) {
+    for (int64_t q = 0; ends < carry_warps(NS); ++q, next += gridDim.x) {
         S& s = ring[q % NS];
         const int64_t id = next < w.total ? next : -1;
-        int v = 0;
-        if (w.ticket && id >= 0 && lane == 0) v = atomicAdd(w.ticket, 1);   // the next tile's, on its way meanwhile
         const TileAt at(a, w, id < 0 ? 0 : id, Bwd);
         int2 range = make_int2(0, 0);
         if (a.cu && id >= 0) range = w.range[at.i];
@@ -359,27 +352,43 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
                 umma::mbar_wait(&ring[k % NS].full, (uint32_t)((k / NS) & 1), a.err, kScanBit);
             return;
         }
-        if (id < 0) ++ends;                      // one for every worker that takes tiles in turn
+        const bool copies = id >= 0 && w.mapped > 0;
         if (lane == 0) {
             s.id = id;
-            if constexpr (Aligned) {
-                if (id >= 0) {
-                    tma::expect_tx(&s.full, S::kCopied);
-                    tma::load_3d(s.la, &maps.la, (int)at.c0, (int)at.t0, (int)at.b, &s.full);
-                    tma::load_3d(s.x, &maps.x, (int)at.c0, (int)at.t0, (int)at.b, &s.full);
-                    if constexpr (Bwd) tma::load_3d(s.y, &maps.y, (int)at.c0, (int)at.t0, (int)at.b, &s.full);
-                } else {
-                    umma::mbar_arrive(&s.full);
-                }
-            } else {
-                umma::mbar_arrive(&s.taken);
-            }
+            umma::mbar_arrive(&s.taken);
+            if (copies) tma::expect_tx(&s.full, S::kCopied);
+            else umma::mbar_arrive(&s.full);
         }
-        if (id >= 0) {
+        __syncwarp();
+        if (copies && lane < R) {
+            // the box of tokens whose index over all rows is `lane` modulo R
+            const int64_t row = (at.row0 - lane + R - 1) >> (Aligned ? 0 : w.log_r);
+            const int64_t x0 = lane * a.D + at.c0;
+            const int box = kTile / R;
+            const int32_t xa = (int32_t)(x0 & ~(int64_t)(S::La::kPer16 - 1)), xx = (int32_t)(x0 & ~(int64_t)(S::X::kPer16 - 1));
+            tma::load_2d(s.la + lane * box * S::La::kPitch, &maps.la, Aligned ? (int32_t)x0 : xa, (int32_t)row, &s.full);
+            tma::load_2d(s.x + lane * box * S::X::kPitch, &maps.x, Aligned ? (int32_t)x0 : xx, (int32_t)row, &s.full);
+            if constexpr (Bwd)
+                tma::load_2d(s.y + lane * box * S::X::kPitch, &maps.y, Aligned ? (int32_t)x0 : xx, (int32_t)row, &s.full);
+        }
+        if (id < 0) {
+            ++ends;                              // one for every worker that takes tiles in turn
+        } else {
+            if constexpr (!Aligned)
+                for (int r = lane; r < kTile; r += 32) {
+                    const int place = (int)((at.row0 + r) & (R - 1));
+                    const int slot = place * (kTile >> w.log_r) + (r >> w.log_r);
+                    const int shift = (int)((place * a.D) & 7);
+                    s.off[r] = (slot * S::La::kPitch + (shift & (S::La::kPer16 - 1)) * 4) |
+                               (slot * S::X::kPitch + (shift & (S::X::kPer16 - 1)) * (int)sizeof(T)) << 16;
+                }
             // sequences that begin or end in the tile
             const bool begins = !a.cu && at.t0 == 0, ends_here = !a.cu && at.t0 + kTile >= a.T;
             const bool marked = a.cu ? range.y > range.x : begins || ends_here;
-            if (lane == 0) s.marked = marked;
+            if (lane == 0) {
+                s.marked = marked;
+                s.plain = !marked && at.t0 + kTile <= a.T && at.row0 + kTile <= w.mapped;
+            }
             if (marked) {
                 for (int t = lane; t < kTile; t += 32) {
                     s.first[t] = begins && t == 0 ? (int)at.b : -1;
@@ -395,35 +404,7 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
         }
         __syncwarp();
         if (lane == 0) umma::mbar_arrive(&s.full);
-        if (w.ticket) next = __shfl_sync(0xffffffffu, v, 0);
-        else next += gridDim.x;
-        if (id < 0) next = w.total;
     }
-}
-
-// A copying warp (unaligned rows): its share of every tile's rows.
-template <typename T, bool Bwd, int NS>
-__device__ __forceinline__ void scan_copy(const GlrArgs& a, const ScanWork& w, Stage<T, false, Bwd>* ring, int share)
-{
-    using S = Stage<T, false, Bwd>;
-    const int64_t total = a.B * a.T * a.D;
-    const int r0 = share * (kTile / kCopyWarps), r1 = r0 + kTile / kCopyWarps;
-    int ends = 0;
-    for (int64_t q = 0; ends < kCarryWarps; ++q) {
-        S& s = ring[q % NS];
-        if (!umma::mbar_wait(&s.taken, (uint32_t)((q / NS) & 1), a.err, kScanBit)) break;
-        if (s.id < 0) {
-            ++ends;
-        } else {
-            const TileAt at(a, w, s.id, Bwd);
-            const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile);
-            S::La::copy(s.la, a.log_a, at.row0, r0, r1, live, a.D, at.c0, total);
-            S::X::copy(s.x, (const T*)a.x, at.row0, r0, r1, live, a.D, at.c0, total);
-            if constexpr (Bwd) S::X::copy(s.y, (const T*)a.dout, at.row0, r0, r1, live, a.D, at.c0, total);
-        }
-        arrive_when_copied(&s.full);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // An aggregator warp: run `run` of every second tile, from tile `group` on.
@@ -433,22 +414,19 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
-    const int dl = (int)(a.D % S::La::kPer16), dx = (int)(a.D % S::X::kPer16);   // shifts from row to row
     for (int64_t q = group;; q += 2) {
         S& s = ring[q % NS];
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
-        int sl = S::La::shift(at.row0 + r0, a.D), sx = S::X::shift(at.row0 + r0, a.D);
         F2 A(1.f, 1.f), B(0.f, 0.f);
-        if (!s.marked) {
+        if (s.plain) {
 #pragma unroll 4
             for (int k = 0; k < kSteps; ++k) {
-                const F2 l = decay2(S::La::get(s.la, r0 + k, sl, lane));
+                const int la = s.la_at(r0 + k);
+                const F2 l = decay2(S::La::get(s.la, la, lane));
                 A = mul2(A, l);
-                B = fma2(l, B, S::X::get(s.x, r0 + k, sx, lane));
-                S::La::put(s.la, r0 + k, sl, lane, l);   // the finishers take the decay from here
-                sl = (sl + dl) % S::La::kPer16;
-                sx = (sx + dx) % S::X::kPer16;
+                B = fma2(l, B, S::X::get(s.x, s.x_at(r0 + k), lane));
+                S::La::put(s.la, la, lane, l);   // the finishers take the decay from here
             }
             if constexpr (Bwd) {
                 *reinterpret_cast<F2*>(&s.fA[run][2 * lane]) = A;
@@ -456,20 +434,19 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
                 // the product of the decays is the same from either end but for its rounding
                 B = F2(0.f, 0.f);
 #pragma unroll 4
-                for (int k = kSteps - 1; k >= 0; --k) {
-                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
-                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
-                    B = mul2(S::La::get(s.la, r0 + k, sl, lane), add2(B, S::X::get(s.y, r0 + k, sx, lane)));
-                }
+                for (int k = kSteps - 1; k >= 0; --k)
+                    B = mul2(S::La::get(s.la, s.la_at(r0 + k), lane), add2(B, S::X::get(s.y, s.x_at(r0 + k), lane)));
             }
         } else {
+            const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile);   // tokens that exist
             const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
             const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
-            for (int k = 0; k < kSteps; ++k) {
-                const int r = r0 + k;
-                F2 l = decay2(S::La::get(s.la, r, sl, lane));
-                const F2 x = S::X::get(s.x, r, sx, lane);
-                const int n = s.first[r];
+            for (int r = r0; r < r0 + kSteps && r < live; ++r) {
+                const bool in = at.row0 + r < w.mapped;
+                const int64_t e = (at.row0 + r) * a.D + c;
+                F2 l = decay2(in ? S::La::get(s.la, s.la_at(r), lane) : S::La::direct(a.log_a + e, on0, on1));
+                const F2 x = in ? S::X::get(s.x, s.x_at(r), lane) : S::X::direct((const T*)a.x + e, on0, on1);
+                const int n = s.marked ? s.first[r] : -1;
                 if (n >= 0) {
                     const int64_t row = Bwd ? n : glr_row(a, n, lane == 0 && at.c0 == 0);
                     const F2 h0 = load_pair<Aligned>(a.h0 && row >= 0 ? a.h0 + row * a.D + c : nullptr, on0, on1);
@@ -485,113 +462,146 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
                     A = mul2(A, l);
                     B = fma2(l, B, x);
                 }
-                S::La::put(s.la, r, sl, lane, l);
-                sl = (sl + dl) % S::La::kPer16;
-                sx = (sx + dx) % S::X::kPer16;
+                S::La::put(s.la, s.la_at(r), lane, l);
             }
             if constexpr (Bwd) {
                 *reinterpret_cast<F2*>(&s.fA[run][2 * lane]) = A;
                 *reinterpret_cast<F2*>(&s.fB[run][2 * lane]) = B;
                 A = F2(1.f, 1.f);
                 B = F2(0.f, 0.f);
-                for (int k = kSteps - 1; k >= 0; --k) {
-                    const int r = r0 + k;
-                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
-                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
-                    const int n = s.last[r];
+                for (int r = (live < r0 + kSteps ? live : r0 + kSteps) - 1; r >= r0; --r) {
+                    const int n = s.marked ? s.last[r] : -1;
                     if (n >= 0) {
                         A = F2(-1.f, -1.f);
                         B = load_pair<Aligned>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
                     }
-                    const F2 l = S::La::get(s.la, r, sl, lane);
+                    const F2 l = S::La::get(s.la, s.la_at(r), lane);
+                    const F2 y = at.row0 + r < w.mapped
+                                     ? S::X::get(s.y, s.x_at(r), lane)
+                                     : S::X::direct((const T*)a.dout + (at.row0 + r) * a.D + c, on0, on1);
                     A = mul2(A, l);
-                    B = mul2(l, add2(B, S::X::get(s.y, r, sx, lane)));
+                    B = mul2(l, add2(B, y));
                 }
             }
         }
         *reinterpret_cast<F2*>(&s.A[run][2 * lane]) = A;
         *reinterpret_cast<F2*>(&s.B[run][2 * lane]) = B;
         // the decays written over log_a come before the TMA copy that fills the stage again
-        if constexpr (Aligned) umma::fence_smem_to_async();
+        umma::fence_smem_to_async();
+        if (run == 0) {
+            // the tile's other runs are there
+            if (!umma::mbar_wait(&s.runs, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
+            float tA[2] = {1.f, 1.f}, tB[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                const int from = Bwd ? kRuns - 1 - k : k;
+                const float2 ra = *reinterpret_cast<const float2*>(&s.A[from][2 * lane]);
+                const float2 rb = *reinterpret_cast<const float2*>(&s.B[from][2 * lane]);
+                tB[0] = leave(ra.x, rb.x, tB[0]);
+                tB[1] = leave(ra.y, rb.y, tB[1]);
+                tA[0] = chain(tA[0], ra.x);
+                tA[1] = chain(tA[1], ra.y);
+            }
+            *reinterpret_cast<float2*>(&s.tA[2 * lane]) = make_float2(tA[0], tA[1]);
+            *reinterpret_cast<float2*>(&s.tB[2 * lane]) = make_float2(tB[0], tB[1]);
+            if (at.order + 1 < w.tiles && at.order % kBlock != kBlock - 1)
+                store_words(w.tile_ab + ((int64_t)at.order * w.cols + at.col) * kCh + 2 * lane, tA, tB);
+        }
         __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&s.agg);
+        if (lane == 0) umma::mbar_arrive(run == 0 ? &s.agg : &s.runs);
     }
 }
 
-// A carrier warp: every third tile, from tile `first` on.
+// `count` (at most N) published words from p on, `pitch` apart: asked for together, and those that
+// are not there yet again together, so that the wait is a few round trips however many are late.
+template <int N>
+__device__ __forceinline__ void await_words(const unsigned long long* p, int64_t pitch, int count,
+                                            unsigned long long (&a)[N], unsigned long long (&b)[N], int* err)
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < count) load_words(p + k * pitch, a[k], b[k]);
+    for (int polls = 0;; ++polls) {
+        unsigned long long there = 1;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < count) there &= a[k] & b[k];
+        if (__all_sync(0xffffffffu, (int)(there & 1))) return;
+        if (polls >= kPolls) {
+            if (err) atomicOr(err, kErrScanWait);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < count && !(a[k] & b[k] & 1)) load_words(p + k * pitch, a[k], b[k]);
+    }
+}
+// The run (A, B) followed by a published one.
+__device__ __forceinline__ void append(float (&A)[2], float (&B)[2], unsigned long long a, unsigned long long b)
+{
+    const float pa[2] = {__uint_as_float((unsigned)a), __uint_as_float((unsigned)b)};
+    B[0] = leave(pa[0], __uint_as_float((unsigned)(a >> 32)), B[0]);
+    B[1] = leave(pa[1], __uint_as_float((unsigned)(b >> 32)), B[1]);
+    A[0] = chain(A[0], pa[0]);
+    A[1] = chain(A[1], pa[1]);
+}
+
+// A carrier warp: one tile of carry_warps(NS), from tile `from` on.
 template <typename T, bool Aligned, bool Bwd, int NS>
 __device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring, int from)
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32;
-    for (int64_t q = from;; q += kCarryWarps) {
+    for (int64_t q = from;; q += carry_warps(NS)) {
         S& s = ring[q % NS];
-        // the end is announced by the loader alone
-        if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
-        if (!umma::mbar_wait(&s.agg, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
+        if (!umma::mbar_wait(&s.taken, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
-        const int64_t g = at.order / kGroup, first = g * kGroup;
-        const int behind = (int)(at.order - first);      // earlier tiles of the group
-        const bool last = behind == kGroup - 1, more = at.order + 1 < w.tiles;
-        float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};
+        const int64_t block = at.order / kBlock, g = block / kBlocks, lane2 = at.col * kCh + 2 * lane;
+        const int blocks = (int)(block % kBlocks), behind = (int)(at.order % kBlock);   // earlier ones of the group, the block
+        const bool more = at.order + 1 < w.tiles, last = behind == kBlock - 1;
+        const int64_t pitch = w.cols * kCh;
+        unsigned long long v0[kBlock], v1[kBlock];
+        // the block's earlier tiles as one run
+        float rA[2] = {1.f, 1.f}, rB[2] = {0.f, 0.f};
+        if (behind > 0) {
+            await_words(w.tile_ab + block * kBlock * pitch + lane2, pitch, behind, v0, v1, a.err);
 #pragma unroll
-        for (int k = 0; k < kRuns; ++k) {
-            const int run = Bwd ? kRuns - 1 - k : k;
-            const float2 ra = *reinterpret_cast<const float2*>(&s.A[run][2 * lane]);
-            const float2 rb = *reinterpret_cast<const float2*>(&s.B[run][2 * lane]);
-            B[0] = leave(ra.x, rb.x, B[0]);
-            B[1] = leave(ra.y, rb.y, B[1]);
-            A[0] = chain(A[0], ra.x);
-            A[1] = chain(A[1], ra.y);
+            for (int k = 0; k < kBlock - 1; ++k)
+                if (k < behind) append(rA, rB, v0[k], v1[k]);
         }
-        if (more && !last) store_words(w.tile_ab + ((int64_t)at.order * w.cols + at.col) * kCh + 2 * lane, A, B);
-        // an entry state is a word of the value and a tag: it is read as soon as it is there, and
-        // asked for now
-        const unsigned long long* entry = w.entry + (g * w.cols + at.col) * kCh + 2 * lane;
-        unsigned long long e0 = 0, e1 = 0;
-        if (g > 0) load_words(entry, e0, e1);
-        // the group's earlier tiles as one run: nothing of it waits for the group's entry state
-        float rA[2] = {1.f, 1.f}, rB[2] = {0.f, 0.f}, carry[2] = {0.f, 0.f};
-        const unsigned long long* ab = w.tile_ab + (first * w.cols + at.col) * kCh + 2 * lane;
-        int polls = 0;
-        for (int k0 = 0; k0 < behind; k0 += kAtOnce) {
-            unsigned long long v0[kAtOnce], v1[kAtOnce];
+        if (!umma::mbar_wait(&s.agg, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
+        const float2 tA = *reinterpret_cast<const float2*>(&s.tA[2 * lane]);
+        const float2 tB = *reinterpret_cast<const float2*>(&s.tB[2 * lane]);
+        const float A[2] = {tA.x, tA.y}, B[2] = {tB.x, tB.y};
+        if (more && last && blocks < kBlocks - 1) {
+            const float bA[2] = {chain(rA[0], A[0]), chain(rA[1], A[1])};
+            const float bB[2] = {leave(A[0], B[0], rB[0]), leave(A[1], B[1], rB[1])};
+            store_words(w.block_ab + block * pitch + lane2, bA, bB);
+        }
+        // the group's entry state, its earlier blocks, then the run
+        float carry[2] = {0.f, 0.f}, pA[2] = {1.f, 1.f}, pB[2] = {0.f, 0.f};
+        if (blocks > 0) {
+            await_words(w.block_ab + (block - blocks) * pitch + lane2, pitch, blocks, v0, v1, a.err);
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                if (k0 + k < behind) load_words(ab + (int64_t)(k0 + k) * w.cols * kCh, v0[k], v1[k]);
+            for (int k = 0; k < kBlocks - 1; ++k)
+                if (k < blocks) append(pA, pB, v0[k], v1[k]);
+        }
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                if (k0 + k < behind) {
-                    while (!(v0[k] & v1[k] & 1)) {
-                        if (++polls >= kPolls) {
-                            if (a.err) atomicOr(a.err, kErrScanWait);
-                            break;
-                        }
-                        load_words(ab + (int64_t)(k0 + k) * w.cols * kCh, v0[k], v1[k]);
-                    }
-                    const float pa[2] = {__uint_as_float((unsigned)v0[k]), __uint_as_float((unsigned)v1[k])};
-                    rB[0] = leave(pa[0], __uint_as_float((unsigned)(v0[k] >> 32)), rB[0]);
-                    rB[1] = leave(pa[1], __uint_as_float((unsigned)(v1[k] >> 32)), rB[1]);
-                    rA[0] = chain(rA[0], pa[0]);
-                    rA[1] = chain(rA[1], pa[1]);
-                }
+        for (int e = 0; e < 2; ++e) {
+            rB[e] = leave(rA[e], rB[e], pB[e]);
+            rA[e] = chain(pA[e], rA[e]);
         }
         if (g > 0) {
-            while (!(e0 & e1 & 1)) {
-                if (++polls >= kPolls) {
-                    if (a.err) atomicOr(a.err, kErrScanWait);
-                    break;
-                }
-                load_words(entry, e0, e1);
-            }
-            carry[0] = __uint_as_float((unsigned)(e0 >> 32));
-            carry[1] = __uint_as_float((unsigned)(e1 >> 32));
+            unsigned long long e0[1], e1[1];
+            await_words(w.entry + g * pitch + lane2, pitch, 1, e0, e1, a.err);
+            carry[0] = __uint_as_float((unsigned)(e0[0] >> 32));
+            carry[1] = __uint_as_float((unsigned)(e1[0] >> 32));
         }
         carry[0] = leave(rA[0], rB[0], carry[0]);
         carry[1] = leave(rA[1], rB[1], carry[1]);
-        if (more && last) {
+        if (more && last && blocks == kBlocks - 1) {
             const float one[2] = {1.f, 1.f}, out[2] = {leave(A[0], B[0], carry[0]), leave(A[1], B[1], carry[1])};
-            store_words(w.entry + ((g + 1) * w.cols + at.col) * kCh + 2 * lane, one, out);
+            store_words(w.entry + (g + 1) * pitch + lane2, one, out);
         }
         *reinterpret_cast<float2*>(&s.carry[2 * lane]) = make_float2(carry[0], carry[1]);
         __syncwarp();
@@ -606,19 +616,22 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
-    const int dl = (int)(a.D % S::La::kPer16), dx = (int)(a.D % S::X::kPer16);
     for (int64_t q = group;; q += 2) {
         S& s = ring[q % NS];
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
-        const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile) - r0;   // tokens of the run that exist
+        const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile);       // tokens that exist
         const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
         const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
         F2 enter(0.f, 0.f);                      // backward: the kept entry state, asked for before the wait
         if constexpr (Bwd) enter = load_pair<Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1);
         if (!umma::mbar_wait(&s.carried, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
-        const bool plain = !s.marked && live >= kSteps;
-        int sl = S::La::shift(at.row0 + r0, a.D), sx = S::X::shift(at.row0 + r0, a.D);
+        const bool marked = s.marked != 0;
+        // x or dout of a token
+        const auto value = [&](const unsigned char* stage, const void* tensor, int r) {
+            return at.row0 + r < w.mapped ? S::X::get(stage, s.x_at(r), lane)
+                                          : S::X::direct((const T*)tensor + (at.row0 + r) * a.D + c, on0, on1);
+        };
         float h[2];
         if constexpr (!Bwd) {
             h[0] = s.carry[2 * lane];
@@ -627,30 +640,25 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 #pragma unroll
                 for (int e = 0; e < 2; ++e) h[e] = leave(s.A[k][2 * lane + e], s.B[k][2 * lane + e], h[e]);
             F2 H(h[0], h[1]);
-            if (a.starts && run == 0 && live > 0 && !(s.marked && s.first[0] >= 0))
+            if (a.starts && run == 0 && !(marked && s.first[0] >= 0))
                 store_pair<float, Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, H);
             T* out = (T*)a.out + (at.row0 + r0) * a.D + c;
-            if (plain && a.out) {
+            if (s.plain && a.out) {
 #pragma unroll 4
-                for (int k = 0; k < kSteps; ++k, out += a.D) {
-                    H = fma2(S::La::get(s.la, r0 + k, sl, lane), H, S::X::get(s.x, r0 + k, sx, lane));
+                for (int r = r0; r < r0 + kSteps; ++r, out += a.D) {
+                    H = fma2(S::La::get(s.la, s.la_at(r), lane), H, S::X::get(s.x, s.x_at(r), lane));
                     store_pair<T, Aligned>(out, on0, on1, H);
-                    sl = (sl + dl) % S::La::kPer16;
-                    sx = (sx + dx) % S::X::kPer16;
                 }
             } else {
-                for (int k = 0; k < live && k < kSteps; ++k, out += a.D) {
-                    const int r = r0 + k;
-                    const F2 l = S::La::get(s.la, r, sl, lane), x = S::X::get(s.x, r, sx, lane);
-                    H = s.marked && s.first[r] >= 0 ? add2(l, x) : fma2(l, H, x);
+                for (int r = r0; r < live && r < r0 + kSteps; ++r, out += a.D) {
+                    const F2 l = S::La::get(s.la, s.la_at(r), lane), x = value(s.x, a.x, r);
+                    H = marked && s.first[r] >= 0 ? add2(l, x) : fma2(l, H, x);
                     if (a.out) store_pair<T, Aligned>(out, on0, on1, H);
-                    const int n = s.marked && a.hT ? s.last[r] : -1;
+                    const int n = marked && a.hT ? s.last[r] : -1;
                     if (n >= 0) {
                         const int64_t row = glr_row(a, n, false);
                         if (row >= 0) store_pair<float, Aligned>(a.hT + row * a.D + c, on0, on1, H);
                     }
-                    sl = (sl + dl) % S::La::kPer16;
-                    sx = (sx + dx) % S::X::kPer16;
                 }
             }
         } else {
@@ -666,50 +674,45 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 #pragma unroll
                 for (int e = 0; e < 2; ++e) g[e] = leave(s.A[k][2 * lane + e], s.B[k][2 * lane + e], g[e]);
             F2 H(h[0], h[1]), G(g[0], g[1]);
-            if (plain) {
+            if (s.plain) {
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
                     before[k] = H;
-                    H = fma2(S::La::get(s.la, r0 + k, sl, lane), H, S::X::get(s.x, r0 + k, sx, lane));
-                    sl = (sl + dl) % S::La::kPer16;
-                    sx = (sx + dx) % S::X::kPer16;
+                    H = fma2(S::La::get(s.la, s.la_at(r0 + k), lane), H, S::X::get(s.x, s.x_at(r0 + k), lane));
                 }
                 T* to = (T*)a.dx + (at.row0 + r0 + kSteps - 1) * a.D + c;
                 float* ta = a.dlog_a + (at.row0 + r0 + kSteps - 1) * a.D + c;
 #pragma unroll
                 for (int k = kSteps - 1; k >= 0; --k, to -= a.D, ta -= a.D) {
-                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
-                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
-                    G = add2(G, S::X::get(s.y, r0 + k, sx, lane));
+                    G = add2(G, S::X::get(s.y, s.x_at(r0 + k), lane));
                     store_pair<T, Aligned>(to, on0, on1, G);
-                    G = mul2(G, S::La::get(s.la, r0 + k, sl, lane));
+                    G = mul2(G, S::La::get(s.la, s.la_at(r0 + k), lane));
                     store_pair<float, Aligned>(ta, on0, on1, mul2(G, before[k]));
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    const int n = s.marked ? s.first[r0 + k] : -1;
+                    const int r = r0 + k;
+                    if (r >= live) break;
+                    const int n = marked ? s.first[r] : -1;
                     if (n >= 0)
                         H = load_pair<Aligned>(a.h0 ? a.h0 + (int64_t)n * a.D + c : nullptr, on0, on1);
                     before[k] = H;
-                    H = fma2(S::La::get(s.la, r0 + k, sl, lane), H, S::X::get(s.x, r0 + k, sx, lane));
-                    sl = (sl + dl) % S::La::kPer16;
-                    sx = (sx + dx) % S::X::kPer16;
+                    H = fma2(S::La::get(s.la, s.la_at(r), lane), H, value(s.x, a.x, r));
                 }
 #pragma unroll
                 for (int k = kSteps - 1; k >= 0; --k) {
-                    sl = (sl + S::La::kPer16 - dl) % S::La::kPer16;
-                    sx = (sx + S::X::kPer16 - dx) % S::X::kPer16;
-                    if (k >= live) continue;
-                    const int n = s.marked ? s.last[r0 + k] : -1;
+                    const int r = r0 + k;
+                    if (r >= live) continue;
+                    const int n = marked ? s.last[r] : -1;
                     if (n >= 0)
                         G = load_pair<Aligned>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
-                    G = add2(G, S::X::get(s.y, r0 + k, sx, lane));
-                    const int64_t to = (at.row0 + r0 + k) * a.D + c;
+                    G = add2(G, value(s.y, a.dout, r));
+                    const int64_t to = (at.row0 + r) * a.D + c;
                     store_pair<T, Aligned>((T*)a.dx + to, on0, on1, G);
-                    G = mul2(G, S::La::get(s.la, r0 + k, sl, lane));
+                    G = mul2(G, S::La::get(s.la, s.la_at(r), lane));
                     store_pair<float, Aligned>(a.dlog_a + to, on0, on1, mul2(G, before[k]));
-                    const int m = s.marked && a.dh0 ? s.first[r0 + k] : -1;
+                    const int m = marked && a.dh0 ? s.first[r] : -1;
                     if (m >= 0) store_pair<float, Aligned>(a.dh0 + (int64_t)m * a.D + c, on0, on1, G);
                 }
             }
@@ -720,21 +723,22 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 }
 
 template <typename T, bool Aligned, bool Bwd>
-__global__ void __launch_bounds__(scan_threads(Aligned), 1)
+__global__ void __launch_bounds__(scan_threads(ring_stages<T, Aligned, Bwd>()), 1)
 glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
 {
     griddep_wait();
     using S = Stage<T, Aligned, Bwd>;
     constexpr int NS = ring_stages<T, Aligned, Bwd>();
-    static_assert(NS > kCarryWarps, "the ends take a stage each");
+    static_assert(NS >= 3, "the ends take a stage each");
     extern __shared__ __align__(128) unsigned char smem[];
     S* ring = reinterpret_cast<S*>(smem);
     int warp = threadIdx.x / 32;
     if (threadIdx.x < NS) {
         S& s = ring[threadIdx.x];
         umma::mbar_init(&s.taken, 1);
-        umma::mbar_init(&s.full, Aligned ? 2 : 1 + 32 * kCopyWarps);   // the marks, and the copies
-        umma::mbar_init(&s.agg, kRuns);
+        umma::mbar_init(&s.full, 2);             // the copies, and the loader's notes
+        umma::mbar_init(&s.runs, kRuns - 1);
+        umma::mbar_init(&s.agg, 1);
         umma::mbar_init(&s.carried, 1);
         umma::mbar_init(&s.empty, kRuns);
         umma::fence_mbar_init();
@@ -744,10 +748,8 @@ glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
     warp -= kAggWarps;
     if (warp < kFinWarps) return scan_finish<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
     warp -= kFinWarps;
-    if (warp < kCarryWarps) return scan_carry<T, Aligned, Bwd, NS>(a, w, ring, warp);
-    warp -= kCarryWarps;
-    if (warp == 0) return scan_load<T, Aligned, Bwd, NS>(a, w, maps, ring);
-    if constexpr (!Aligned) scan_copy<T, Bwd, NS>(a, w, ring, warp - 1);
+    if (warp < carry_warps(NS)) return scan_carry<T, Aligned, Bwd, NS>(a, w, ring, warp);
+    scan_load<T, Aligned, Bwd, NS>(a, w, maps, ring);
 }
 
 template <typename T>
@@ -782,19 +784,22 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
     w.cols = a.B * ((a.D + kCh - 1) / kCh);
     w.tiles = (a.T + kTile - 1) / kTile;
     w.total = w.tiles * w.cols;
+    w.blocks = (uint32_t)((a.D + kCh - 1) / kCh);
+    w.by_cols = Divide(w.cols);
+    w.by_blocks = Divide(w.blocks);
     StreamBuffer buf;
-    // a single tile per column waits for nothing: no ticket, no setup, unless offsets or
-    // sequences without tokens want looking at
+    // a single tile per column waits for nothing: no setup, unless offsets or sequences without
+    // tokens want looking at
     if (w.tiles > 1 || a.cu || a.T == 0) {
-        const int64_t groups = (w.tiles + kGroup - 1) / kGroup;
-        const int64_t words = (groups * w.cols + w.total) * kCh, ranges = (w.tiles + 1) / 2 * 2;
-        const cudaError_t e = buf.alloc((size_t)(16 + (words + ranges) * 8), st);
+        const int64_t blocks = (w.tiles + kBlock - 1) / kBlock, groups = (blocks + kBlocks - 1) / kBlocks;
+        const int64_t words = ((groups + blocks) * w.cols + w.total) * kCh, ranges = (w.tiles + 1) / 2 * 2;
+        const cudaError_t e = buf.alloc((size_t)((words + ranges) * 8), st);
         if (e != cudaSuccess) return e;
-        w.ticket = static_cast<int*>(buf.ptr);
-        w.entry = reinterpret_cast<unsigned long long*>(w.ticket + 4);
-        w.tile_ab = w.entry + groups * w.cols * kCh;
+        w.entry = static_cast<unsigned long long*>(buf.ptr);
+        w.block_ab = w.entry + groups * w.cols * kCh;
+        w.tile_ab = w.block_ab + blocks * w.cols * kCh;
         w.range = reinterpret_cast<int2*>(w.tile_ab + w.total * kCh);
-        w.zeroed = 1 + words / 2;
+        w.zeroed = w.tiles > 1 ? words / 2 : 0;
         const int64_t work = w.zeroed / 8 + (a.cu ? w.tiles : 0) + (a.cu || a.T == 0 ? a.N * 32 : 0);
         const int64_t ctas = (work + 255) / 256;
         LaunchScope scope(st, K_GLR_SETUP);
@@ -807,17 +812,29 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
     const auto kernel = glr_scan_kernel<T, Aligned, Bwd>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // rows of R tokens have a stride of 16 bytes
+    constexpr bool bf16 = sizeof(T) == 2;
+    if (!Aligned) w.log_r = a.D * (int64_t)sizeof(T) % 8 == 0 ? 1 : a.D * (int64_t)sizeof(T) % 4 == 0 ? 2 : 3;
+    const int64_t R = int64_t(1) << w.log_r, rows = a.B * a.T / R;
+    w.mapped = rows * R;
     ScanMaps maps = {};
-    if (Aligned) {
-        constexpr bool bf16 = sizeof(T) == 2;
-        cudaError_t m = make_tensor_map_3d(&maps.la, a.log_a, false, a.D, a.T, a.B, kCh, kTile);
-        if (m == cudaSuccess) m = make_tensor_map_3d(&maps.x, a.x, bf16, a.D, a.T, a.B, kCh, kTile);
-        if (m == cudaSuccess && Bwd) m = make_tensor_map_3d(&maps.y, a.dout, bf16, a.D, a.T, a.B, kCh, kTile);
+    if (rows > 0) {
+        using S = Stage<T, Aligned, Bwd>;
+        const auto map = [&](CUtensorMap* m, const void* p, bool half, int pitch) {
+            const int e = half ? 2 : 4;
+            return make_tensor_map_2d(m, p, half, (uint64_t)(R * a.D), (uint64_t)rows, (uint64_t)(R * a.D * e),
+                                      (uint32_t)(pitch / e), (uint32_t)(kTile / R), false);
+        };
+        cudaError_t m = map(&maps.la, a.log_a, false, S::La::kPitch);
+        if (m == cudaSuccess) m = map(&maps.x, a.x, bf16, S::X::kPitch);
+        if (m == cudaSuccess && Bwd) m = map(&maps.y, a.dout, bf16, S::X::kPitch);
         if (m != cudaSuccess) return m;
     }
     LaunchScope scope(st, Bwd ? K_GLR_BWD : K_GLR_FWD);
-    return launch_pdl(kernel, dim3((unsigned)(w.total < kSMs ? w.total : kSMs)), dim3(scan_threads(Aligned)), smem, st,
-                      a, w, maps);
+    const int64_t sms = device_sm_count();
+    const dim3 grid((unsigned)(w.total < sms ? w.total : sms)), block(scan_threads(ring_stages<T, Aligned, Bwd>()));
+    if (w.tiles == 1) return launch_pdl(glr_scan_kernel<T, Aligned, Bwd>, grid, block, smem, st, a, w, maps);
+    return launch_coop(kernel, grid, block, smem, st, a, w, maps);
 }
 
 template <bool Bwd>
@@ -855,7 +872,8 @@ namespace {
 
 // Channels of one call: grid.y and the 32-bit tile arithmetic of the kernels.
 constexpr int64_t kMaxChannels = int64_t(1) << 20;
-constexpr int64_t kMaxTokens = int64_t(1) << 40;
+constexpr int64_t kMaxTokens = 0x7fffffffLL - 2 * kTile;   // 32-bit coordinates
+constexpr int64_t kMaxRows = int64_t(1) << 40;
 
 // Rows, channels and tokens; `rows` = 1 with cu_seqlens.
 kda_status_t glr_check_sizes(int64_t B, int64_t T, int64_t D, kda_io_dtype_t io, bool packed)
@@ -863,8 +881,8 @@ kda_status_t glr_check_sizes(int64_t B, int64_t T, int64_t D, kda_io_dtype_t io,
     if (B < 0 || T < 0 || D < 0) return KDA_ERR_INVALID_ARG;
     if (io != KDA_IO_F32 && io != KDA_IO_BF16) return KDA_ERR_UNSUPPORTED;
     if (D > kMaxChannels || B > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-    if (T > 0x7fffffffLL || (B > 0 && T > kMaxTokens / B)) return KDA_ERR_UNSUPPORTED;
-    // tickets and offsets are 32-bit
+    if (T > kMaxTokens || (B > 0 && T > kMaxTokens / B)) return KDA_ERR_UNSUPPORTED;
+    // tile numbers are 32-bit
     const int64_t cols = (packed ? 1 : B) * ((D + kCh - 1) / kCh);
     if (cols > 0 && (T + kTile - 1) / kTile > (0x7fffffffLL - 65536) / cols) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
@@ -906,7 +924,7 @@ kda_status_t glr_step_impl(const void* x, const float* log_a, float* state, cons
 {
     if (N < 0 || P < 0 || D < 0) return KDA_ERR_INVALID_ARG;
     if (io != KDA_IO_F32 && io != KDA_IO_BF16) return KDA_ERR_UNSUPPORTED;
-    if (D > kMaxChannels || N > 0x7fffffffLL || P > kMaxTokens) return KDA_ERR_UNSUPPORTED;
+    if (D > kMaxChannels || N > 0x7fffffffLL || P > kMaxRows) return KDA_ERR_UNSUPPORTED;
     if (N == 0 || D == 0) return KDA_OK;
     if (!tensor_ok(x) || !tensor_ok(log_a) || !tensor_ok(out)) return KDA_ERR_INVALID_ARG;
     if (!(P == 0 && slots) && !tensor_ok(state)) return KDA_ERR_INVALID_ARG;
@@ -939,7 +957,7 @@ kda_status_t kda_glr_scan_fwd_slots(const void* x, const float* log_a, float* st
                                     int64_t D, kda_io_dtype_t io_dtype, cudaStream_t stream)
 {
     if (slots == nullptr || P < 0 || (P > 0 && state_pool == nullptr)) return KDA_ERR_INVALID_ARG;
-    if (P > kMaxTokens) return KDA_ERR_UNSUPPORTED;
+    if (P > kMaxRows) return KDA_ERR_UNSUPPORTED;
     return glr_fwd_impl(x, log_a, state_pool, out, state_pool, starts, slots, P, cu_seqlens, B, T, D,
                         io_dtype, stream);
 }

@@ -286,6 +286,25 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return e != cudaSuccess ? e : g;
 }
 
+// Launch of a grid whose blocks wait on one another: all of them are resident, or the launch fails.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_coop(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+    const cudaError_t g = cudaGetLastError();
+    return e != cudaSuccess ? e : g;
+}
+
 // Opened around every kernel launch: counts it and, while the profiler is
 // enabled, records start/stop CUDA events on the launching stream.
 class LaunchScope {
@@ -394,7 +413,6 @@ struct GlrArgs {
     kda_io_dtype_t io;
     int* err;
 };
-constexpr int kSMs = 148;     // of a B200: CTAs of a persistent grid
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st);
 cudaError_t launch_glr_step(const void* x, const float* log_a, float* state, const int32_t* slots,

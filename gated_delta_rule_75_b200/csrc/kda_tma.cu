@@ -44,21 +44,4 @@ cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, ui
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t cols, uint64_t rows,
-                               uint64_t planes, uint32_t box_cols, uint32_t box_rows)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return cudaErrorNotSupported;
-    const uint64_t row_bytes = cols * (bf16 ? 2 : 4);
-    const cuuint64_t dims[3] = {cols, rows, planes};
-    const cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
-    const cuuint32_t box[3] = {box_cols, box_rows, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                          3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace kda

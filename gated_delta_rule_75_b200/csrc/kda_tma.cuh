@@ -22,20 +22,6 @@ __device__ __forceinline__ void load_2d(void* dst_smem, const CUtensorMap* map, 
         : "memory");
 }
 
-// 3-D tiled load of a one-plane box at (x = innermost element index, y = row, z = plane).
-__device__ __forceinline__ void load_3d(void* dst_smem, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
-                                        uint64_t* bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];"
-        :
-        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),
-          "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z),
-          "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar)))
-        : "memory");
-}
-
 // Untiled bulk copy global -> shared, completion on `bar`.
 __device__ __forceinline__ void load_bulk(void* dst_smem, const void* src, uint32_t bytes,
                                           uint64_t* bar)
@@ -85,10 +71,5 @@ __device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes)
 cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, uint64_t cols,
                                uint64_t rows, uint64_t row_bytes, uint32_t box_cols,
                                uint32_t box_rows, bool swizzle128);
-
-// Host: a contiguous 3-D tensor [planes][rows][cols], tiled in boxes of one plane,
-// box_rows x box_cols, no swizzle; what lies outside the tensor reads as zeros.
-cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t cols, uint64_t rows,
-                               uint64_t planes, uint32_t box_cols, uint32_t box_rows);
 
 }  // namespace kda

@@ -421,8 +421,8 @@ KDA_API kda_status_t kda_affine_prefix(const float* maps, const float* offs, con
  *              the token in no sequence.)
  *  cu_seqlens  as for kda_chunk_fwd (x, log_a, out and starts then have a leading axis
  *              of 1, B is the number of sequences, N = B)
- * Any D >= 1 up to 2^20 (rows of D a multiple of 4 are moved in wide accesses); D, B
- * or T of 0 is a no-op apart from hT = h0.  The state is fp32 throughout; out is
+ * Any D >= 1 up to 2^20, fewer than 2^31 - 128 tokens in all; D, B or T of 0 is a no-op
+ * apart from hT = h0.  The state is fp32 throughout; out is
  * rounded once.  A call over more than one tile of the token axis uses a workspace of
  * about 9 bytes per tile and channel from the library's pool.  The result is the same
  * on every run.
