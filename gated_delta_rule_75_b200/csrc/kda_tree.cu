@@ -10,6 +10,21 @@
 // so no node's state is ever formed, and S0 is read once for all of them.  The products of
 // decays come from walking up the path one factor at a time: every factor is at most 1, so any
 // decay rate is safe, and the last one is the row that multiplies S0.
+//
+// Bound by memory: a head's state is 64 KiB at d = 128, its 16 drafted tokens 24 KiB; next to
+// that 1 MFLOP of products with S0, which would take as long on the fp32 cores.  One CTA of 256
+// threads for one (sequence, head), two or more of them on an SM so that one's loads cover
+// another's arithmetic:
+//   1. alpha, k into shared memory (S0, v on their way into the L2); depths, order by depth;
+//   2. eight lanes a node walk up its path, every lane 16 (8) channels: the dots with every
+//      ancestor (three shuffles each), then the node's two rows, kept in registers;
+//   3. the rows (keys, then queries) as bf16 summands in shared memory, and their product with
+//      S0 on mma.sync (m16n8k16): S0 goes from memory to B fragments in registers, no copy in
+//      shared memory, a warp 32 columns and half of the rows.  Rows and S0 are split into two
+//      bf16 summands each (three for fp32 I/O) and the products down to 2^-17 (2^-25) of the
+//      whole are summed in fp32.  tcgen05 would want both operands staged for M = 128 rows
+//      whatever the tree; here the tensor work is a third of the memory time;
+//   4. level by level, a warp a node: u_i and o_i.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -26,35 +41,72 @@ __device__ __forceinline__ int tree_parent(const int32_t* parents, int i, int* e
     return p;
 }
 
-__device__ __forceinline__ float warp_sum(float v)
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One CTA of 256 threads for one (sequence, head).
-template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(256) tree_fwd_kernel(TreeArgs a)
+// Four channels of q, k or v.
+template <typename T> __device__ __forceinline__ float4 load4(const T* p);
+template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p)
 {
-    constexpr int CPL = DK / 32;
-    extern __shared__ float sm[];
-    const int K = (int)a.K;
-    float* alpha = sm;                       // [K][DK]
-    float* kk = alpha + K * DK;              // [K][DK]
-    float* W = kk + K * DK;                  // [2K][DK]: decayed keys, decayed queries
-    float* AB = W + 2 * K * DK;              // [K][K][2]: by place on the path, self at 0
-    float* bet = AB + 2 * K * K;             // [K]
-    int* par = reinterpret_cast<int*>(bet + K);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// (x, y) as NS bf16 pairs whose sum is within 2^-(8 NS + 1) of each: s[0] the largest.
+template <int NS>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&s)[NS])
+{
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        s[i] = pack_bf16(x, y);
+        x -= __uint_as_float(s[i] << 16);
+        y -= __uint_as_float(s[i] & 0xffff0000u);
+    }
+}
+
+// Shared memory of a CTA for trees of up to KB nodes.
+template <int DK, int DV, int KB, int NS>
+struct TreeSmem {
+    static constexpr int kPitch = DK + 16;                 // bf16 elements of a row: rows 8 banks apart
+    static constexpr int kPairs = KB * (KB + 1) / 2;
+    static constexpr int kA = 2 * KB * DK * 4, kB = NS * 2 * KB * kPitch * 2, kC = 2 * KB * DV * 4;
+    static constexpr int kRegion = kA > kB ? (kA > kC ? kA : kC) : (kB > kC ? kB : kC);
+    // alpha, k [KB][DK]; then the rows [NS][2 KB][kPitch]; then the products with S0 [2][KB][DV],
+    // of which the first half becomes u
+    alignas(16) unsigned char region[kRegion];
+    float2 ab[kPairs];                                     // A, B of a node, by place on its path, itself at 0
+    float beta[KB];
+    int par[KB], depth[KB], off[KB], order[KB], level_end[KB + 1];
+    unsigned char anc[kPairs];                             // the node at that place
+};
+
+template <typename T, int DK, int DV, int KB>
+__global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArgs a)
+{
+    constexpr int NS = sizeof(T) == 2 ? 2 : 3;
+    using Smem = TreeSmem<DK, DV, KB, NS>;
+    constexpr int kQuads = DK / 32;                        // float4 channel groups of a lane in the walk
+    constexpr int kPerGroup = (KB + 31) / 32;              // nodes of a group of eight lanes
+    extern __shared__ __align__(16) unsigned char raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(raw);
+    float* alpha = reinterpret_cast<float*>(sm.region);
+    float* kf = alpha + KB * DK;
+    const int K = (int)a.K, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int64_t n = blockIdx.x / a.H, h = blockIdx.x % a.H;
 
-    int live = K;
-    if (a.num_nodes) {
-        live = a.num_nodes[n];
-        if ((live < 0 || live > K) && tid == 0) atomicOr(a.err, kErrSeqlens);
-        live = live < 0 ? 0 : live > K ? K : live;
-    }
     int64_t row = n;
     if (a.slots) {
         row = a.slots[n];
@@ -62,73 +114,251 @@ __global__ void __launch_bounds__(256) tree_fwd_kernel(TreeArgs a)
         if (row >= a.P) row = -1;
     }
     const float* S0 = row < 0 ? nullptr : a.state + (row * a.H + h) * (int64_t)DK * DV;
-    const int64_t tok0 = (n * K) * a.H + h;  // node i: tok0 + i * H
-    for (int i = tid; i < live; i += 256) {
-        par[i] = tree_parent(a.parents + n * K, i, a.err);
-        bet[i] = a.beta[tok0 + i * a.H];
+    if (S0 && tid == 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S0), "n"(DK * DV * 4) : "memory");
+    int live = K;
+    if (a.num_nodes) {
+        live = a.num_nodes[n];
+        if ((live < 0 || live > K) && tid == 0) atomicOr(a.err, kErrSeqlens);
+        live = live < 0 ? 0 : live > K ? K : live;
     }
-    for (int i = tid; i < live * DK; i += 256) {
-        const int64_t at = (tok0 + (i / DK) * a.H) * DK + i % DK;
-        alpha[i] = expf(a.log_alpha[at]);
-        kk[i] = IO<T>::load((const T*)a.k, at);
+    if (live == 0) return;
+    const int64_t tok0 = (n * K) * a.H + h;                // node i: tok0 + i * H
+    if (tid < live) {
+        sm.par[tid] = tree_parent(a.parents + n * K, tid, a.err);
+        sm.beta[tid] = a.beta[tok0 + tid * a.H];
+        asm volatile("prefetch.global.L2 [%0];" ::"l"((const T*)a.v + (tok0 + tid * a.H) * DV));
+        if (DV * sizeof(T) > 128) asm volatile("prefetch.global.L2 [%0];" ::"l"((const T*)a.v + (tok0 + tid * a.H) * DV + DV / 2));
     }
-    __syncthreads();
-    for (int i = warp; i < live; i += 8) {   // one warp walks up one node's path
-        float wk[CPL], wq[CPL], dot = 0.f;
-#pragma unroll
-        for (int r = 0; r < CPL; ++r) {
-            const int c = r * 32 + lane;
-            const float q = IO<T>::load((const T*)a.q, (tok0 + i * a.H) * DK + c);
-            dot += q * kk[i * DK + c];
-            wk[r] = kk[i * DK + c] * alpha[i * DK + c];
-            wq[r] = q * alpha[i * DK + c];
-        }
-        dot = warp_sum(dot);
-        if (lane == 0) AB[2 * (i * K) + 1] = dot;
-        int place = 1;
-        for (int j = par[i]; j >= 0; j = par[j], ++place) {
-            float x = 0.f, y = 0.f;
-#pragma unroll
-            for (int r = 0; r < CPL; ++r) {
-                const int c = r * 32 + lane;
-                x += wk[r] * kk[j * DK + c];
-                y += wq[r] * kk[j * DK + c];
-                wk[r] *= alpha[j * DK + c];
-                wq[r] *= alpha[j * DK + c];
-            }
-            x = warp_sum(x);
-            y = warp_sum(y);
-            if (lane == 0) {
-                AB[2 * (i * K + place)] = x;
-                AB[2 * (i * K + place) + 1] = y;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < CPL; ++r) {
-            W[i * DK + r * 32 + lane] = wk[r];
-            W[(K + i) * DK + r * 32 + lane] = wq[r];
-        }
+    if (tid <= KB) sm.level_end[tid] = 0;
+    for (int e = tid; e < live * (DK / 4); e += 256) {
+        const int i = e / (DK / 4), c = e % (DK / 4) * 4;
+        const int64_t at = (tok0 + i * a.H) * DK + c;
+        const float4 g = *reinterpret_cast<const float4*>(a.log_alpha + at);
+        const float4 k = load4((const T*)a.k + at);
+        *reinterpret_cast<float4*>(alpha + i * DK + c) = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+        *reinterpret_cast<float4*>(kf + i * DK + c) = k;
     }
     __syncthreads();
-    // one thread a column of S0: the products, then the nodes in order
-    if (tid >= DV) return;
-    float u[64];
-    for (int i = 0; i < live; ++i) {
-        float pk = 0.f, pq = 0.f;
-        if (S0)
-            for (int c = 0; c < DK; ++c) {
-                const float s = S0[c * DV + tid];
-                pk += W[i * DK + c] * s;
-                pq += W[(K + i) * DK + c] * s;
-            }
-        int place = 1;
-        for (int j = par[i]; j >= 0; j = par[j], ++place) {
-            pk += AB[2 * (i * K + place)] * u[j];
-            pq += AB[2 * (i * K + place) + 1] * u[j];
+    if (tid < live) {
+        int d = 1;                                         // nodes on the path, itself too
+        for (int j = sm.par[tid]; j >= 0; j = sm.par[j]) ++d;
+        sm.depth[tid] = d;
+    }
+    __syncthreads();
+    if (tid < live) {
+        const int mine = sm.depth[tid];
+        int off = 0, pos = 0;
+        for (int j = 0; j < live; ++j) {
+            const int d = sm.depth[j];
+            off += j < tid ? d : 0;
+            pos += d < mine || (d == mine && j < tid);
         }
-        const int64_t at = (tok0 + i * a.H) * DV + tid;
-        u[i] = bet[i] * (IO<T>::load((const T*)a.v, at) - pk);
-        IO<T>::store((T*)a.out, at, a.scale * (pq + AB[2 * (i * K) + 1] * u[i]));
+        sm.off[tid] = off;
+        sm.order[pos] = tid;
+        atomicMax(&sm.level_end[mine], pos + 1);
+    }
+    __syncthreads();
+
+    // 2. the walks: lane l of a group holds channels 4 (l + 8 m) .. + 3
+    const int l8 = lane % 8;
+    float4 wk[kPerGroup][kQuads], wq[kPerGroup][kQuads];
+    int node[kPerGroup];
+#pragma unroll
+    for (int r = 0; r < kPerGroup; ++r) {
+        const int at = r * 32 + warp * 4 + lane / 8;
+        const int i = at < live ? sm.order[at] : -1;
+        node[r] = i;
+        int j = -1, place = 0;
+        float2 dot = make_float2(0.f, 0.f);
+        if (i >= 0) {
+            j = sm.par[i];
+            place = sm.off[i];
+#pragma unroll
+            for (int m = 0; m < kQuads; ++m) {
+                const int c = 4 * (l8 + 8 * m);
+                const float4 q = load4((const T*)a.q + (tok0 + i * a.H) * DK + c);
+                const float4 k = *reinterpret_cast<const float4*>(kf + i * DK + c);
+                const float4 g = *reinterpret_cast<const float4*>(alpha + i * DK + c);
+                dot.y += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+                wk[r][m] = make_float4(k.x * g.x, k.y * g.y, k.z * g.z, k.w * g.w);
+                wq[r][m] = make_float4(q.x * g.x, q.y * g.y, q.z * g.z, q.w * g.w);
+            }
+        }
+        int at_node = i;                                   // the node whose dots are in `dot`
+        // every lane of the warp goes round as often as its longest path asks
+        while (__any_sync(0xffffffffu, at_node >= 0)) {
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                dot.x += __shfl_xor_sync(0xffffffffu, dot.x, o);
+                dot.y += __shfl_xor_sync(0xffffffffu, dot.y, o);
+            }
+            if (at_node >= 0 && l8 == 0) {
+                sm.ab[place] = dot;
+                sm.anc[place] = (unsigned char)at_node;
+            }
+            ++place;
+            at_node = j;
+            if (j >= 0) {
+                dot = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < kQuads; ++m) {
+                    const int c = 4 * (l8 + 8 * m);
+                    const float4 k = *reinterpret_cast<const float4*>(kf + j * DK + c);
+                    const float4 g = *reinterpret_cast<const float4*>(alpha + j * DK + c);
+                    float4 &x = wk[r][m], &y = wq[r][m];
+                    dot.x += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
+                    dot.y += y.x * k.x + y.y * k.y + y.z * k.z + y.w * k.w;
+                    x.x *= g.x; x.y *= g.y; x.z *= g.z; x.w *= g.w;
+                    y.x *= g.x; y.y *= g.y; y.z *= g.z; y.w *= g.w;
+                }
+                j = sm.par[j];
+            }
+        }
+    }
+    __syncthreads();                                       // alpha and k are done with
+
+    // 3. the rows times S0
+    float* prod = reinterpret_cast<float*>(sm.region);
+    if (S0) {
+        constexpr int P = Smem::kPitch;
+        __nv_bfloat16* W = reinterpret_cast<__nv_bfloat16*>(sm.region);
+#pragma unroll
+        for (int r = 0; r < kPerGroup; ++r)
+            if (node[r] >= 0)
+#pragma unroll
+                for (int m = 0; m < kQuads; ++m)
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+                        const float4 x = which ? wq[r][m] : wk[r][m];
+                        uint32_t lo[NS], hi[NS];
+                        split<NS>(x.x, x.y, lo);
+                        split<NS>(x.z, x.w, hi);
+#pragma unroll
+                        for (int s = 0; s < NS; ++s)
+                            *reinterpret_cast<uint2*>(W + (s * 2 * KB + which * KB + node[r]) * P + 4 * (l8 + 8 * m)) =
+                                make_uint2(lo[s], hi[s]);
+                    }
+        __syncthreads();
+        constexpr int kColGroups = DV / 32, kRowGroups = 8 / kColGroups, kTiles = 2 * KB / 16;
+        constexpr int kMine = (kTiles + kRowGroups - 1) / kRowGroups;      // row tiles of a warp
+        const int cols = warp % kColGroups * 32, rows = warp / kColGroups;
+        const int g = lane / 4, t = lane % 4;
+        float acc[kMine][4][4];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+        // lane (g, t): rows 4 t .. 4 t + 3 of a block of 16 (the same order on both sides), columns
+        // 4 g .. 4 g + 3 of the warp's, one for each of four MMAs
+        const float* from = S0 + 4 * t * DV + cols + 4 * g;
+        float4 s[4], next[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const float4*>(from + i * DV);
+#pragma unroll 2
+        for (int k0 = 0; k0 < DK; k0 += 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[i] = next[i];
+                if (k0 + 16 < DK) next[i] = *reinterpret_cast<const float4*>(from + (k0 + 16 + i) * DV);
+            }
+            uint32_t b0[4][NS], b1[4][NS];
+            split<NS>(s[0].x, s[1].x, b0[0]); split<NS>(s[2].x, s[3].x, b1[0]);
+            split<NS>(s[0].y, s[1].y, b0[1]); split<NS>(s[2].y, s[3].y, b1[1]);
+            split<NS>(s[0].z, s[1].z, b0[2]); split<NS>(s[2].z, s[3].z, b1[2]);
+            split<NS>(s[0].w, s[1].w, b0[3]); split<NS>(s[2].w, s[3].w, b1[3]);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int tile = rows + i * kRowGroups;
+                // tiles that hold no node: none of the keys' or the queries' rows
+                if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
+#pragma unroll
+                for (int sa = 0; sa < NS; ++sa) {
+                    const __nv_bfloat16* w = W + (sa * 2 * KB + tile * 16 + g) * P + k0 + 4 * t;
+                    const uint2 x = *reinterpret_cast<const uint2*>(w), y = *reinterpret_cast<const uint2*>(w + 8 * P);
+#pragma unroll
+                    for (int sb = 0; sb < NS - sa; ++sb)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma_16816(acc[i][j], x.x, y.x, x.y, y.y, b0[j][sb], b1[j][sb]);
+                }
+            }
+        }
+        __syncthreads();                                   // the rows are done with
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int tile = rows + i * kRowGroups;
+            if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float* to = prod + (tile * 16 + g + 8 * half) * DV + cols + 8 * t;
+                *reinterpret_cast<float4*>(to) = make_float4(acc[i][0][2 * half], acc[i][1][2 * half], acc[i][2][2 * half],
+                                                             acc[i][3][2 * half]);
+                *reinterpret_cast<float4*>(to + 4) = make_float4(acc[i][0][2 * half + 1], acc[i][1][2 * half + 1],
+                                                                 acc[i][2][2 * half + 1], acc[i][3][2 * half + 1]);
+            }
+        }
+    } else {
+        for (int e = tid; e < 2 * KB * DV; e += 256) prod[e] = 0.f;
+    }
+    __syncthreads();
+
+    // 4. level by level; a lane holds CPL columns
+    constexpr int CPL = DV / 32;
+    struct alignas(4 * CPL) Cols { float v[CPL]; };
+    for (int done = 0, level = 1; done < live; ++level) {
+        const int end = sm.level_end[level];
+        for (int at = done + warp; at < end; at += 8) {
+            const int i = sm.order[at], off = sm.off[i];
+            Cols pk = *reinterpret_cast<const Cols*>(prod + i * DV + CPL * lane);
+            Cols pq = *reinterpret_cast<const Cols*>(prod + (KB + i) * DV + CPL * lane);
+            const int64_t to = (tok0 + i * a.H) * DV + CPL * lane;
+            Cols v;
+            if constexpr (sizeof(T) == 4) {
+                v = *reinterpret_cast<const Cols*>((const T*)a.v + to);
+            } else {
+                uint32_t u[CPL / 2];
+                if constexpr (CPL == 4) {
+                    const uint2 w = *reinterpret_cast<const uint2*>((const T*)a.v + to);
+                    u[0] = w.x; u[1] = w.y;
+                } else {
+                    u[0] = *reinterpret_cast<const uint32_t*>((const T*)a.v + to);
+                }
+#pragma unroll
+                for (int e = 0; e < CPL; e += 2) {
+                    v.v[e] = __uint_as_float(u[e / 2] << 16);
+                    v.v[e + 1] = __uint_as_float(u[e / 2] & 0xffff0000u);
+                }
+            }
+#pragma unroll 4
+            for (int p = 1; p < level; ++p) {
+                const float2 ab = sm.ab[off + p];
+                const Cols u = *reinterpret_cast<const Cols*>(prod + sm.anc[off + p] * DV + CPL * lane);
+#pragma unroll
+                for (int e = 0; e < CPL; ++e) {
+                    pk.v[e] += ab.x * u.v[e];
+                    pq.v[e] += ab.y * u.v[e];
+                }
+            }
+            const float self = sm.ab[off].y, b = sm.beta[i];
+            Cols o;
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) {
+                pk.v[e] = b * (v.v[e] - pk.v[e]);
+                o.v[e] = a.scale * (pq.v[e] + self * pk.v[e]);
+            }
+            *reinterpret_cast<Cols*>(prod + i * DV + CPL * lane) = pk;
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<Cols*>((T*)a.out + to) = o;
+            } else if constexpr (CPL == 4) {
+                *reinterpret_cast<uint2*>((T*)a.out + to) = make_uint2(pack_bf16(o.v[0], o.v[1]), pack_bf16(o.v[2], o.v[3]));
+            } else {
+                *reinterpret_cast<uint32_t*>((T*)a.out + to) = pack_bf16(o.v[0], o.v[1]);
+            }
+        }
+        done = end;
+        __syncthreads();
     }
 }
 
@@ -204,16 +434,25 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(TreeArgs a)
 
 namespace {
 
+template <typename T, int DK, int DV, int KB>
+cudaError_t tree_fwd_kb(const TreeArgs& a, cudaStream_t st)
+{
+    constexpr int smem = (int)sizeof(TreeSmem<DK, DV, KB, sizeof(T) == 2 ? 2 : 3>);
+    const cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T, DK, DV, KB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    LaunchScope scope(st, K_TREE_FWD);
+    tree_fwd_kernel<T, DK, DV, KB><<<(unsigned)(a.N * a.H), 256, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, int DK, int DV>
 cudaError_t tree_fwd_t(const TreeArgs& a, cudaStream_t st)
 {
-    const size_t smem = (size_t)(4 * a.K * DK + 2 * a.K * a.K + a.K) * 4 + (size_t)a.K * 4;
-    const cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T, DK, DV>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    LaunchScope scope(st, K_TREE_FWD);
-    tree_fwd_kernel<T, DK, DV><<<(unsigned)(a.N * a.H), 256, smem, st>>>(a);
-    return cudaGetLastError();
+    // shared memory and registers for the next power of two of nodes
+    if (a.K <= 16) return tree_fwd_kb<T, DK, DV, 16>(a, st);
+    if (a.K <= 32) return tree_fwd_kb<T, DK, DV, 32>(a, st);
+    return tree_fwd_kb<T, DK, DV, 64>(a, st);
 }
 
 template <typename T, int DK, int DV>
