@@ -127,17 +127,33 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
     if (tid < live) {
         sm.par[tid] = tree_parent(a.parents + n * K, tid, a.err);
         sm.beta[tid] = a.beta[tok0 + tid * a.H];
-        asm volatile("prefetch.global.L2 [%0];" ::"l"((const T*)a.v + (tok0 + tid * a.H) * DV));
-        if (DV * sizeof(T) > 128) asm volatile("prefetch.global.L2 [%0];" ::"l"((const T*)a.v + (tok0 + tid * a.H) * DV + DV / 2));
+        // q and v are asked for when a node's turn comes: into the L2 meanwhile
+#pragma unroll
+        for (int c = 0; c < DK * (int)sizeof(T); c += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.q + (tok0 + tid * a.H) * DK * sizeof(T) + c));
+#pragma unroll
+        for (int c = 0; c < DV * (int)sizeof(T); c += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.v + (tok0 + tid * a.H) * DV * sizeof(T) + c));
     }
     if (tid <= KB) sm.level_end[tid] = 0;
-    for (int e = tid; e < live * (DK / 4); e += 256) {
-        const int i = e / (DK / 4), c = e % (DK / 4) * 4;
-        const int64_t at = (tok0 + i * a.H) * DK + c;
-        const float4 g = *reinterpret_cast<const float4*>(a.log_alpha + at);
-        const float4 k = load4((const T*)a.k + at);
-        *reinterpret_cast<float4*>(alpha + i * DK + c) = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
-        *reinterpret_cast<float4*>(kf + i * DK + c) = k;
+    constexpr int kAhead = KB >= 32 ? 4 : 2;               // quads of alpha and k a thread has on their way
+    for (int e0 = tid; e0 < live * (DK / 4); e0 += 256 * kAhead) {
+        float4 g[kAhead], k[kAhead];
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            const int e = e0 + r * 256, i = e / (DK / 4), c = e % (DK / 4) * 4;
+            if (e >= live * (DK / 4)) break;
+            const int64_t at = (tok0 + i * a.H) * DK + c;
+            g[r] = __ldcs(reinterpret_cast<const float4*>(a.log_alpha + at));
+            k[r] = load4((const T*)a.k + at);
+        }
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            const int e = e0 + r * 256;
+            if (e >= live * (DK / 4)) break;
+            *reinterpret_cast<float4*>(alpha + 4 * e) = make_float4(expf(g[r].x), expf(g[r].y), expf(g[r].z), expf(g[r].w));
+            *reinterpret_cast<float4*>(kf + 4 * e) = k[r];
+        }
     }
     __syncthreads();
     if (tid < live) {
@@ -240,51 +256,61 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
                                 make_uint2(lo[s], hi[s]);
                     }
         __syncthreads();
-        constexpr int kColGroups = DV / 32, kRowGroups = 8 / kColGroups, kTiles = 2 * KB / 16;
+        // a warp's columns and row tiles: 16 columns leave no row tiles to a second warp that would
+        // read S0 again; with 64 nodes the rows would then be read by twice as many warps
+        constexpr int VW = KB <= 32 ? 2 : 4, kCols = 8 * VW;
+        constexpr int kColGroups = DV / kCols, kRowGroups = 8 / kColGroups, kTiles = 2 * KB / 16;
         constexpr int kMine = (kTiles + kRowGroups - 1) / kRowGroups;      // row tiles of a warp
-        const int cols = warp % kColGroups * 32, rows = warp / kColGroups;
+        constexpr int kDeep = KB <= 32 ? 4 : 2;                            // blocks of S0 on their way
+        struct alignas(4 * VW) Quad { float v[VW]; };
+        const int cols = warp % kColGroups * kCols, rows = warp / kColGroups;
         const int g = lane / 4, t = lane % 4;
-        float acc[kMine][4][4];
+        float acc[kMine][VW][4];
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < VW; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
         // lane (g, t): rows 4 t .. 4 t + 3 of a block of 16 (the same order on both sides), columns
-        // 4 g .. 4 g + 3 of the warp's, one for each of four MMAs
-        const float* from = S0 + 4 * t * DV + cols + 4 * g;
-        float4 s[4], next[4];
+        // VW g .. of the warp's, one for each of VW MMAs
+        const float* from = S0 + 4 * t * DV + cols + VW * g;
+        Quad s[kDeep][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const float4*>(from + i * DV);
-#pragma unroll 2
-        for (int k0 = 0; k0 < DK; k0 += 16) {
+        for (int d = 0; d < kDeep; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[i] = next[i];
-                if (k0 + 16 < DK) next[i] = *reinterpret_cast<const float4*>(from + (k0 + 16 + i) * DV);
-            }
-            uint32_t b0[4][NS], b1[4][NS];
-            split<NS>(s[0].x, s[1].x, b0[0]); split<NS>(s[2].x, s[3].x, b1[0]);
-            split<NS>(s[0].y, s[1].y, b0[1]); split<NS>(s[2].y, s[3].y, b1[1]);
-            split<NS>(s[0].z, s[1].z, b0[2]); split<NS>(s[2].z, s[3].z, b1[2]);
-            split<NS>(s[0].w, s[1].w, b0[3]); split<NS>(s[2].w, s[3].w, b1[3]);
+            for (int i = 0; i < 4; ++i) s[d][i] = *reinterpret_cast<const Quad*>(from + (16 * d + i) * DV);
+#pragma unroll 1
+        for (int kd = 0; kd < DK; kd += 16 * kDeep)
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int tile = rows + i * kRowGroups;
-                // tiles that hold no node: none of the keys' or the queries' rows
-                if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
+            for (int d = 0; d < kDeep; ++d) {
+                const int k0 = kd + 16 * d;
+                uint32_t b0[VW][NS], b1[VW][NS];
 #pragma unroll
-                for (int sa = 0; sa < NS; ++sa) {
-                    const __nv_bfloat16* w = W + (sa * 2 * KB + tile * 16 + g) * P + k0 + 4 * t;
-                    const uint2 x = *reinterpret_cast<const uint2*>(w), y = *reinterpret_cast<const uint2*>(w + 8 * P);
+                for (int j = 0; j < VW; ++j) {
+                    split<NS>(s[d][0].v[j], s[d][1].v[j], b0[j]);
+                    split<NS>(s[d][2].v[j], s[d][3].v[j], b1[j]);
+                }
+                if (k0 + 16 * kDeep < DK)
 #pragma unroll
-                    for (int sb = 0; sb < NS - sa; ++sb)
+                    for (int i = 0; i < 4; ++i)
+                        s[d][i] = *reinterpret_cast<const Quad*>(from + (k0 + 16 * kDeep + i) * DV);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma_16816(acc[i][j], x.x, y.x, x.y, y.y, b0[j][sb], b1[j][sb]);
+                for (int i = 0; i < kMine; ++i) {
+                    const int tile = rows + i * kRowGroups;
+                    // tiles that hold no node: none of the keys' or the queries' rows
+                    if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
+#pragma unroll
+                    for (int sa = 0; sa < NS; ++sa) {
+                        const __nv_bfloat16* w = W + (sa * 2 * KB + tile * 16 + g) * P + k0 + 4 * t;
+                        const uint2 x = *reinterpret_cast<const uint2*>(w), y = *reinterpret_cast<const uint2*>(w + 8 * P);
+#pragma unroll
+                        for (int sb = 0; sb < NS - sa; ++sb)
+#pragma unroll
+                            for (int j = 0; j < VW; ++j) mma_16816(acc[i][j], x.x, y.x, x.y, y.y, b0[j][sb], b1[j][sb]);
+                    }
                 }
             }
-        }
         __syncthreads();                                   // the rows are done with
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -292,11 +318,15 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
             if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float* to = prod + (tile * 16 + g + 8 * half) * DV + cols + 8 * t;
-                *reinterpret_cast<float4*>(to) = make_float4(acc[i][0][2 * half], acc[i][1][2 * half], acc[i][2][2 * half],
-                                                             acc[i][3][2 * half]);
-                *reinterpret_cast<float4*>(to + 4) = make_float4(acc[i][0][2 * half + 1], acc[i][1][2 * half + 1],
-                                                                 acc[i][2][2 * half + 1], acc[i][3][2 * half + 1]);
+                Quad lo, hi;
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                    lo.v[j] = acc[i][j][2 * half];
+                    hi.v[j] = acc[i][j][2 * half + 1];
+                }
+                float* to = prod + (tile * 16 + g + 8 * half) * DV + cols + 2 * VW * t;
+                *reinterpret_cast<Quad*>(to) = lo;
+                *reinterpret_cast<Quad*>(to + VW) = hi;
             }
         }
     } else {
@@ -307,30 +337,36 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
     // 4. level by level; a lane holds CPL columns
     constexpr int CPL = DV / 32;
     struct alignas(4 * CPL) Cols { float v[CPL]; };
+    // v of the warp's first node of a level is asked for one level before
+    const auto load_v = [&](int at) {
+        Cols v = {};
+        if (at < live) {
+            const T* p = (const T*)a.v + (tok0 + sm.order[at] * a.H) * DV + CPL * lane;
+            if constexpr (sizeof(T) == 4) {
+                v = *reinterpret_cast<const Cols*>(p);
+            } else {
+                struct alignas(2 * CPL) Raw { uint32_t u[CPL / 2]; };
+                const Raw r = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+                for (int e = 0; e < CPL; e += 2) {
+                    v.v[e] = __uint_as_float(r.u[e / 2] << 16);
+                    v.v[e + 1] = __uint_as_float(r.u[e / 2] & 0xffff0000u);
+                }
+            }
+        }
+        return v;
+    };
+    Cols ahead = load_v(warp);
     for (int done = 0, level = 1; done < live; ++level) {
         const int end = sm.level_end[level];
+        const Cols first = ahead;
+        ahead = load_v(end + warp);
         for (int at = done + warp; at < end; at += 8) {
+            const Cols v = at == done + warp ? first : load_v(at);
             const int i = sm.order[at], off = sm.off[i];
             Cols pk = *reinterpret_cast<const Cols*>(prod + i * DV + CPL * lane);
             Cols pq = *reinterpret_cast<const Cols*>(prod + (KB + i) * DV + CPL * lane);
             const int64_t to = (tok0 + i * a.H) * DV + CPL * lane;
-            Cols v;
-            if constexpr (sizeof(T) == 4) {
-                v = *reinterpret_cast<const Cols*>((const T*)a.v + to);
-            } else {
-                uint32_t u[CPL / 2];
-                if constexpr (CPL == 4) {
-                    const uint2 w = *reinterpret_cast<const uint2*>((const T*)a.v + to);
-                    u[0] = w.x; u[1] = w.y;
-                } else {
-                    u[0] = *reinterpret_cast<const uint32_t*>((const T*)a.v + to);
-                }
-#pragma unroll
-                for (int e = 0; e < CPL; e += 2) {
-                    v.v[e] = __uint_as_float(u[e / 2] << 16);
-                    v.v[e + 1] = __uint_as_float(u[e / 2] & 0xffff0000u);
-                }
-            }
 #pragma unroll 4
             for (int p = 1; p < level; ++p) {
                 const float2 ab = sm.ab[off + p];
