@@ -430,6 +430,7 @@ struct TreeArgs {
     const int32_t* accepted;    // [N] (tree_commit)
     void* out;
     int64_t N, P, K, H;
+    int64_t resident;           // CTAs that run at once (tree_fwd)
     int dk, dv;
     float scale;
     kda_io_dtype_t io;

@@ -12,21 +12,21 @@
 // decay rate is safe, and the last one is the row that multiplies S0.
 //
 // Bound by memory: a head's state is 64 KiB at d = 128, its 16 drafted tokens 24 KiB; next to
-// that 1 MFLOP of products with S0, which would take as long on the fp32 cores.  One CTA of 256
-// threads for one (sequence, head), two or more of them on an SM so that one's loads cover
-// another's arithmetic:
-//   1. alpha, k into shared memory (S0, v on their way into the L2); depths, order by depth;
+// that 1 MFLOP of products with S0 (4 for 64 nodes), which mma.sync took 1.6 (6.5) us of an SM for,
+// so they are on tcgen05: 0.3 (0.8) us.  One CTA of 384 threads for one (sequence, head), two of
+// them on an SM up to 32 nodes so that one's loads cover another's arithmetic.  Warps 0 - 7:
+//   1. alpha, k into shared memory (q, v on their way into the L2); depths, order by depth;
 //   2. eight lanes a node walk up its path, every lane 16 (8) channels: the dots with every
 //      ancestor (three shuffles each), then the node's two rows, kept in registers;
-//   3. the rows (keys, then queries) as bf16 summands in shared memory, and their product with
-//      S0 on mma.sync (m16n8k16): S0 goes from memory to B fragments in registers, no copy in
-//      shared memory, a warp 32 columns and half of the rows.  Rows and S0 are split into two
-//      bf16 summands each (three for fp32 I/O) and the products down to 2^-17 (2^-25) of the
-//      whole are summed in fp32.  tcgen05 would want both operands staged for M = 128 rows
-//      whatever the tree; here the tensor work is a third of the memory time;
-//   4. level by level, a warp a node: u_i and o_i.
+//   3. the rows (keys, then queries) as bf16 summands in shared memory.
+// Meanwhile warps 8 - 11 bring S0 there, as bf16 summands too.  Then one thread issues the
+// product, transposed, D^T = S0^T rows^T: M = dv, N = rows, so that N and the tensor memory follow
+// the number of nodes.  Rows and S0 are split into two bf16 summands each (three for fp32 I/O) and
+// the products down to 2^-17 (2^-25) of the whole are summed in fp32.  Then, all warps:
+//   4. D^T to shared memory; level by level, a warp a node: u_i and o_i.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_umma.cuh"
 
 namespace kda {
 
@@ -41,15 +41,6 @@ __device__ __forceinline__ int tree_parent(const int32_t* parents, int i, int* e
     return p;
 }
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // Four channels of q, k or v.
 template <typename T> __device__ __forceinline__ float4 load4(const T* p);
 template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -59,11 +50,7 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xffff0000u));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
+using umma::pack_bf16;
 
 // (x, y) as NS bf16 pairs whose sum is within 2^-(8 NS + 1) of each: s[0] the largest.
 template <int NS>
@@ -77,30 +64,63 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&s)[NS])
     }
 }
 
+constexpr int kTreeThreads = 384, kTreeWalkers = 256;
+constexpr int kTreeErrBit = 2;                             // "operand MMAs" of the error word
+
 // Shared memory of a CTA for trees of up to KB nodes.
 template <int DK, int DV, int KB, int NS>
 struct TreeSmem {
-    static constexpr int kPitch = DK + 16;                 // bf16 elements of a row: rows 8 banks apart
     static constexpr int kPairs = KB * (KB + 1) / 2;
-    static constexpr int kA = 2 * KB * DK * 4, kB = NS * 2 * KB * kPitch * 2, kC = 2 * KB * DV * 4;
+    static constexpr int kState = DK * DV * 2;             // bytes of one summand of S0
+    // with dv = 64 the upper half of the M = 128 operand is whatever follows: its rows are not used
+    static constexpr int kSlack = DV == 64 ? DK * 128 : 0;
+    static constexpr int kA = 2 * KB * DK * 4, kB = NS * 2 * KB * DK * 2, kC = 2 * KB * DV * 4;
     static constexpr int kRegion = kA > kB ? (kA > kC ? kA : kC) : (kB > kC ? kB : kC);
-    // alpha, k [KB][DK]; then the rows [NS][2 KB][kPitch]; then the products with S0 [2][KB][DV],
-    // of which the first half becomes u
-    alignas(16) unsigned char region[kRegion];
+    // S0: [NS] of blocks of 64 columns, [DK][64] bf16 each, 128-byte swizzle (M-major operand)
+    alignas(1024) unsigned char state[NS * kState + kSlack];
+    // alpha, k [KB][DK]; then the rows, [NS] of blocks of 64 channels, [2 KP][64] bf16 each, 128-byte
+    // swizzle (K-major operand); then the products with S0 [2][KB][DV], whose first half becomes u
+    alignas(1024) unsigned char region[kRegion];
     float2 ab[kPairs];                                     // A, B of a node, by place on its path, itself at 0
     float beta[KB];
     int par[KB], depth[KB], off[KB], order[KB], level_end[KB + 1];
+    uint64_t done;                                         // the product
+    uint32_t tmem;
     unsigned char anc[kPairs];                             // the node at that place
 };
 
+template <int Bytes> __device__ __forceinline__ void prefetch_l2(const void* p)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "n"(Bytes) : "memory");
+}
+
+// Everything that the CTA of sequence n, head h reads, by 128 threads.
+template <typename T, int DK, int DV>
+__device__ __forceinline__ void prefetch_item(const TreeArgs& a, int64_t n, int64_t h, int tid)
+{
+    const int64_t row = a.slots ? a.slots[n] : n;
+    const int live = a.num_nodes ? a.num_nodes[n] : (int)a.K;
+    if (tid == 127 && row >= 0 && row < a.P) prefetch_l2<DK * DV * 4>(a.state + (row * a.H + h) * (int64_t)DK * DV);
+    if (tid >= live || tid >= a.K) return;
+    const int64_t tok = (n * a.K + tid) * a.H + h;
+    prefetch_l2<DK * 4>(a.log_alpha + tok * DK);
+    prefetch_l2<DK * sizeof(T)>((const T*)a.k + tok * DK);
+    prefetch_l2<DK * sizeof(T)>((const T*)a.q + tok * DK);
+    prefetch_l2<DV * sizeof(T)>((const T*)a.v + tok * DV);
+}
+
+// Warps 0 - 7 only.
+__device__ __forceinline__ void walkers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTreeWalkers) : "memory"); }
+
 template <typename T, int DK, int DV, int KB>
-__global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArgs a)
+__global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 : 1) tree_fwd_kernel(const TreeArgs a)
 {
     constexpr int NS = sizeof(T) == 2 ? 2 : 3;
     using Smem = TreeSmem<DK, DV, KB, NS>;
     constexpr int kQuads = DK / 32;                        // float4 channel groups of a lane in the walk
     constexpr int kPerGroup = (KB + 31) / 32;              // nodes of a group of eight lanes
-    extern __shared__ __align__(16) unsigned char raw[];
+    constexpr int kColumns = 2 * KB < 32 ? 32 : 2 * KB;    // of tensor memory
+    extern __shared__ __align__(1024) unsigned char raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     float* alpha = reinterpret_cast<float*>(sm.region);
     float* kf = alpha + KB * DK;
@@ -114,8 +134,6 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
         if (row >= a.P) row = -1;
     }
     const float* S0 = row < 0 ? nullptr : a.state + (row * a.H + h) * (int64_t)DK * DV;
-    if (S0 && tid == 0)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S0), "n"(DK * DV * 4) : "memory");
     int live = K;
     if (a.num_nodes) {
         live = a.num_nodes[n];
@@ -124,247 +142,240 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
     }
     if (live == 0) return;
     const int64_t tok0 = (n * K) * a.H + h;                // node i: tok0 + i * H
-    if (tid < live) {
-        sm.par[tid] = tree_parent(a.parents + n * K, tid, a.err);
-        sm.beta[tid] = a.beta[tok0 + tid * a.H];
-        // q and v are asked for when a node's turn comes: into the L2 meanwhile
-#pragma unroll
-        for (int c = 0; c < DK * (int)sizeof(T); c += 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.q + (tok0 + tid * a.H) * DK * sizeof(T) + c));
-#pragma unroll
-        for (int c = 0; c < DV * (int)sizeof(T); c += 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.v + (tok0 + tid * a.H) * DV * sizeof(T) + c));
+    const int KP = (live + 15) / 16 * 16;                  // rows of keys, and of queries
+    if (warp == 8) {
+        umma::tmem_alloc(&sm.tmem, kColumns);
+        umma::tmem_relinquish();
     }
-    if (tid <= KB) sm.level_end[tid] = 0;
-    constexpr int kAhead = KB >= 32 ? 4 : 2;               // quads of alpha and k a thread has on their way
-    for (int e0 = tid; e0 < live * (DK / 4); e0 += 256 * kAhead) {
-        float4 g[kAhead], k[kAhead];
+    if (tid == 0) {
+        umma::mbar_init(&sm.done, 1);
+        umma::fence_mbar_init();
+    }
+    float* prod = reinterpret_cast<float*>(sm.region);
+    if (warp >= 8) {
+        // S0: a row (two rows of 64 columns) a warp at a time
+        constexpr int kLoads = 8, kPerRow = DV / 4, kStep = (kTreeThreads - kTreeWalkers) / kPerRow;
+        const int mine = tid - kTreeWalkers, c = mine % kPerRow * 4, r0 = mine / kPerRow;
+        if (S0)
+            for (int k0 = r0; k0 < DK; k0 += kLoads * kStep) {
+                float4 s[kLoads];
 #pragma unroll
-        for (int r = 0; r < kAhead; ++r) {
-            const int e = e0 + r * 256, i = e / (DK / 4), c = e % (DK / 4) * 4;
-            if (e >= live * (DK / 4)) break;
-            const int64_t at = (tok0 + i * a.H) * DK + c;
-            g[r] = __ldcs(reinterpret_cast<const float4*>(a.log_alpha + at));
-            k[r] = load4((const T*)a.k + at);
+                for (int i = 0; i < kLoads; ++i)
+                    s[i] = __ldcs(reinterpret_cast<const float4*>(S0 + (k0 + i * kStep) * DV + c));
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    uint32_t lo[NS], hi[NS];
+                    split<NS>(s[i].x, s[i].y, lo);
+                    split<NS>(s[i].z, s[i].w, hi);
+                    const uint32_t to = c / 64 * (DK * 128) + umma::sw128_offset(k0 + i * kStep, c % 64);
+#pragma unroll
+                    for (int e = 0; e < NS; ++e)
+                        *reinterpret_cast<uint2*>(sm.state + e * Smem::kState + to) = make_uint2(lo[e], hi[e]);
+                }
+            }
+        // what the CTA that follows this one on the SM will read goes into the L2 meanwhile, or memory
+        // would idle while this one computes
+        const int64_t next = (int64_t)blockIdx.x + a.resident;
+        if (next < a.N * a.H) prefetch_item<T, DK, DV>(a, next / a.H, next % a.H, mine);
+    } else {
+        if (tid < live) {
+            sm.par[tid] = tree_parent(a.parents + n * K, tid, a.err);
+            sm.beta[tid] = a.beta[tok0 + tid * a.H];
+            // q and v are asked for when a node's turn comes: into the L2 meanwhile
+#pragma unroll
+            for (int c = 0; c < DK * (int)sizeof(T); c += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.q + (tok0 + tid * a.H) * DK * sizeof(T) + c));
+#pragma unroll
+            for (int c = 0; c < DV * (int)sizeof(T); c += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.v + (tok0 + tid * a.H) * DV * sizeof(T) + c));
         }
+        if (tid <= KB) sm.level_end[tid] = 0;
+        constexpr int kAhead = KB >= 32 ? 4 : 2;               // quads of alpha and k a thread has on their way
+        for (int e0 = tid; e0 < live * (DK / 4); e0 += kTreeWalkers * kAhead) {
+            float4 g[kAhead], k[kAhead];
 #pragma unroll
-        for (int r = 0; r < kAhead; ++r) {
-            const int e = e0 + r * 256;
-            if (e >= live * (DK / 4)) break;
-            *reinterpret_cast<float4*>(alpha + 4 * e) = make_float4(expf(g[r].x), expf(g[r].y), expf(g[r].z), expf(g[r].w));
-            *reinterpret_cast<float4*>(kf + 4 * e) = k[r];
+            for (int r = 0; r < kAhead; ++r) {
+                const int e = e0 + r * kTreeWalkers, i = e / (DK / 4), c = e % (DK / 4) * 4;
+                if (e >= live * (DK / 4)) break;
+                const int64_t at = (tok0 + i * a.H) * DK + c;
+                g[r] = __ldcs(reinterpret_cast<const float4*>(a.log_alpha + at));
+                k[r] = load4((const T*)a.k + at);
+            }
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r) {
+                const int e = e0 + r * kTreeWalkers;
+                if (e >= live * (DK / 4)) break;
+                *reinterpret_cast<float4*>(alpha + 4 * e) = make_float4(expf(g[r].x), expf(g[r].y), expf(g[r].z), expf(g[r].w));
+                *reinterpret_cast<float4*>(kf + 4 * e) = k[r];
+            }
         }
-    }
-    __syncthreads();
-    if (tid < live) {
-        int d = 1;                                         // nodes on the path, itself too
-        for (int j = sm.par[tid]; j >= 0; j = sm.par[j]) ++d;
-        sm.depth[tid] = d;
-    }
-    __syncthreads();
-    if (tid < live) {
-        const int mine = sm.depth[tid];
-        int off = 0, pos = 0;
-        for (int j = 0; j < live; ++j) {
-            const int d = sm.depth[j];
-            off += j < tid ? d : 0;
-            pos += d < mine || (d == mine && j < tid);
+        walkers_sync();
+        if (tid < live) {
+            int d = 1;                                         // nodes on the path, itself too
+            for (int j = sm.par[tid]; j >= 0; j = sm.par[j]) ++d;
+            sm.depth[tid] = d;
         }
-        sm.off[tid] = off;
-        sm.order[pos] = tid;
-        atomicMax(&sm.level_end[mine], pos + 1);
-    }
-    __syncthreads();
+        walkers_sync();
+        if (tid < live) {
+            const int mine = sm.depth[tid];
+            int off = 0, pos = 0;
+            for (int j = 0; j < live; ++j) {
+                const int d = sm.depth[j];
+                off += j < tid ? d : 0;
+                pos += d < mine || (d == mine && j < tid);
+            }
+            sm.off[tid] = off;
+            sm.order[pos] = tid;
+            atomicMax(&sm.level_end[mine], pos + 1);
+        }
+        walkers_sync();
 
-    // 2. the walks: lane l of a group holds channels 4 (l + 8 m) .. + 3
-    const int l8 = lane % 8;
-    float4 wk[kPerGroup][kQuads], wq[kPerGroup][kQuads];
-    int node[kPerGroup];
+        // 2. the walks: lane l of a group holds channels 4 (l + 8 m) .. + 3
+        const int l8 = lane % 8;
+        float4 wk[kPerGroup][kQuads], wq[kPerGroup][kQuads];
+        int node[kPerGroup];
 #pragma unroll
-    for (int r = 0; r < kPerGroup; ++r) {
-        const int at = r * 32 + warp * 4 + lane / 8;
-        const int i = at < live ? sm.order[at] : -1;
-        node[r] = i;
-        int j = -1, place = 0;
-        float2 dot = make_float2(0.f, 0.f);
-        if (i >= 0) {
-            j = sm.par[i];
-            place = sm.off[i];
-#pragma unroll
-            for (int m = 0; m < kQuads; ++m) {
-                const int c = 4 * (l8 + 8 * m);
-                const float4 q = load4((const T*)a.q + (tok0 + i * a.H) * DK + c);
-                const float4 k = *reinterpret_cast<const float4*>(kf + i * DK + c);
-                const float4 g = *reinterpret_cast<const float4*>(alpha + i * DK + c);
-                dot.y += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-                wk[r][m] = make_float4(k.x * g.x, k.y * g.y, k.z * g.z, k.w * g.w);
-                wq[r][m] = make_float4(q.x * g.x, q.y * g.y, q.z * g.z, q.w * g.w);
-            }
-        }
-        int at_node = i;                                   // the node whose dots are in `dot`
-        // every lane of the warp goes round as often as its longest path asks
-        while (__any_sync(0xffffffffu, at_node >= 0)) {
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) {
-                dot.x += __shfl_xor_sync(0xffffffffu, dot.x, o);
-                dot.y += __shfl_xor_sync(0xffffffffu, dot.y, o);
-            }
-            if (at_node >= 0 && l8 == 0) {
-                sm.ab[place] = dot;
-                sm.anc[place] = (unsigned char)at_node;
-            }
-            ++place;
-            at_node = j;
-            if (j >= 0) {
-                dot = make_float2(0.f, 0.f);
+        for (int r = 0; r < kPerGroup; ++r) {
+            const int at = r * 32 + warp * 4 + lane / 8;
+            const int i = at < live ? sm.order[at] : -1;
+            node[r] = i;
+            int j = -1, place = 0;
+            float2 dot = make_float2(0.f, 0.f);
+            if (i >= 0) {
+                j = sm.par[i];
+                place = sm.off[i];
 #pragma unroll
                 for (int m = 0; m < kQuads; ++m) {
                     const int c = 4 * (l8 + 8 * m);
-                    const float4 k = *reinterpret_cast<const float4*>(kf + j * DK + c);
-                    const float4 g = *reinterpret_cast<const float4*>(alpha + j * DK + c);
-                    float4 &x = wk[r][m], &y = wq[r][m];
-                    dot.x += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
-                    dot.y += y.x * k.x + y.y * k.y + y.z * k.z + y.w * k.w;
-                    x.x *= g.x; x.y *= g.y; x.z *= g.z; x.w *= g.w;
-                    y.x *= g.x; y.y *= g.y; y.z *= g.z; y.w *= g.w;
+                    const float4 q = load4((const T*)a.q + (tok0 + i * a.H) * DK + c);
+                    const float4 k = *reinterpret_cast<const float4*>(kf + i * DK + c);
+                    const float4 g = *reinterpret_cast<const float4*>(alpha + i * DK + c);
+                    dot.y += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+                    wk[r][m] = make_float4(k.x * g.x, k.y * g.y, k.z * g.z, k.w * g.w);
+                    wq[r][m] = make_float4(q.x * g.x, q.y * g.y, q.z * g.z, q.w * g.w);
                 }
-                j = sm.par[j];
+            }
+            int at_node = i;                                   // the node whose dots are in `dot`
+            // every lane of the warp goes round as often as its longest path asks
+            while (__any_sync(0xffffffffu, at_node >= 0)) {
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) {
+                    dot.x += __shfl_xor_sync(0xffffffffu, dot.x, o);
+                    dot.y += __shfl_xor_sync(0xffffffffu, dot.y, o);
+                }
+                if (at_node >= 0 && l8 == 0) {
+                    sm.ab[place] = dot;
+                    sm.anc[place] = (unsigned char)at_node;
+                }
+                ++place;
+                at_node = j;
+                if (j >= 0) {
+                    dot = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int m = 0; m < kQuads; ++m) {
+                        const int c = 4 * (l8 + 8 * m);
+                        const float4 k = *reinterpret_cast<const float4*>(kf + j * DK + c);
+                        const float4 g = *reinterpret_cast<const float4*>(alpha + j * DK + c);
+                        float4 &x = wk[r][m], &y = wq[r][m];
+                        dot.x += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
+                        dot.y += y.x * k.x + y.y * k.y + y.z * k.z + y.w * k.w;
+                        x.x *= g.x; x.y *= g.y; x.z *= g.z; x.w *= g.w;
+                        y.x *= g.x; y.y *= g.y; y.z *= g.z; y.w *= g.w;
+                    }
+                    j = sm.par[j];
+                }
             }
         }
-    }
-    __syncthreads();                                       // alpha and k are done with
+        walkers_sync();                                        // alpha and k are done with
 
-    // 3. the rows times S0
-    float* prod = reinterpret_cast<float*>(sm.region);
+        // 3. the rows
+        if (S0) {
+#pragma unroll
+            for (int r = 0; r < kPerGroup; ++r)
+                if (node[r] >= 0)
+#pragma unroll
+                    for (int m = 0; m < kQuads; ++m)
+#pragma unroll
+                        for (int which = 0; which < 2; ++which) {
+                            const float4 x = which ? wq[r][m] : wk[r][m];
+                            uint32_t lo[NS], hi[NS];
+                            split<NS>(x.x, x.y, lo);
+                            split<NS>(x.z, x.w, hi);
+                            const int c = 4 * (l8 + 8 * m);
+                            const uint32_t to = c / 64 * (2 * KP * 128) + umma::sw128_offset(which * KP + node[r], c % 64);
+#pragma unroll
+                            for (int e = 0; e < NS; ++e)
+                                *reinterpret_cast<uint2*>(sm.region + e * (2 * KP * DK * 2) + to) = make_uint2(lo[e], hi[e]);
+                        }
+        }
+    }
+    umma::fence_smem_to_async();
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    bool fine = true;
     if (S0) {
-        constexpr int P = Smem::kPitch;
-        __nv_bfloat16* W = reinterpret_cast<__nv_bfloat16*>(sm.region);
+        if (tid == 0) {
+            const uint32_t idesc = umma::make_idesc_bf16(128, 2 * KP, true, false);
+            const uint64_t ad = umma::make_desc(umma::smem_u32(sm.state), DK * 128, 1024);
+            const uint64_t bd = umma::make_desc(umma::smem_u32(sm.region), 16, 1024);
+            const uint32_t block = 2 * KP * 128 / 16;      // of the rows' channels, in descriptor units
 #pragma unroll
-        for (int r = 0; r < kPerGroup; ++r)
-            if (node[r] >= 0)
+            for (int sa = 0; sa < NS; ++sa)                // summand of S0, of the rows
 #pragma unroll
-                for (int m = 0; m < kQuads; ++m)
+                for (int sb = 0; sb < NS - sa; ++sb)
 #pragma unroll
-                    for (int which = 0; which < 2; ++which) {
-                        const float4 x = which ? wq[r][m] : wk[r][m];
-                        uint32_t lo[NS], hi[NS];
-                        split<NS>(x.x, x.y, lo);
-                        split<NS>(x.z, x.w, hi);
+                    for (int ks = 0; ks < DK / 16; ++ks)
+                        umma::mma_bf16(sm.tmem, ad + (sa * Smem::kState + ks * 2048) / 16,
+                                       bd + (sb * (DK / 64) + ks / 4) * block + ks % 4 * 2, idesc, sa + sb + ks > 0);
+            umma::commit(&sm.done);
+        }
+    }
+    // a thread's column and its first 16 rows: v is asked for before the wait.  Lane = column of S0,
+    // TMEM column = row; the warps of one quarter of the lanes take 16 rows in turn
+    const int col = warp % 4 * 32 + lane;
+    T v0[16];
+    const auto load_v = [&](int r0, T (&v)[16]) {
 #pragma unroll
-                        for (int s = 0; s < NS; ++s)
-                            *reinterpret_cast<uint2*>(W + (s * 2 * KB + which * KB + node[r]) * P + 4 * (l8 + 8 * m)) =
-                                make_uint2(lo[s], hi[s]);
-                    }
-        __syncthreads();
-        // a warp's columns and row tiles: 16 columns leave no row tiles to a second warp that would
-        // read S0 again; with 64 nodes the rows would then be read by twice as many warps
-        constexpr int VW = KB <= 32 ? 2 : 4, kCols = 8 * VW;
-        constexpr int kColGroups = DV / kCols, kRowGroups = 8 / kColGroups, kTiles = 2 * KB / 16;
-        constexpr int kMine = (kTiles + kRowGroups - 1) / kRowGroups;      // row tiles of a warp
-        constexpr int kDeep = KB <= 32 ? 4 : 2;                            // blocks of S0 on their way
-        struct alignas(4 * VW) Quad { float v[VW]; };
-        const int cols = warp % kColGroups * kCols, rows = warp / kColGroups;
-        const int g = lane / 4, t = lane % 4;
-        float acc[kMine][VW][4];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i)
-#pragma unroll
-            for (int j = 0; j < VW; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-        // lane (g, t): rows 4 t .. 4 t + 3 of a block of 16 (the same order on both sides), columns
-        // VW g .. of the warp's, one for each of VW MMAs
-        const float* from = S0 + 4 * t * DV + cols + VW * g;
-        Quad s[kDeep][4];
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[d][i] = *reinterpret_cast<const Quad*>(from + (16 * d + i) * DV);
-#pragma unroll 1
-        for (int kd = 0; kd < DK; kd += 16 * kDeep)
-#pragma unroll
-            for (int d = 0; d < kDeep; ++d) {
-                const int k0 = kd + 16 * d;
-                uint32_t b0[VW][NS], b1[VW][NS];
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    split<NS>(s[d][0].v[j], s[d][1].v[j], b0[j]);
-                    split<NS>(s[d][2].v[j], s[d][3].v[j], b1[j]);
-                }
-                if (k0 + 16 * kDeep < DK)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[d][i] = *reinterpret_cast<const Quad*>(from + (k0 + 16 * kDeep + i) * DV);
-#pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    const int tile = rows + i * kRowGroups;
-                    // tiles that hold no node: none of the keys' or the queries' rows
-                    if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
-#pragma unroll
-                    for (int sa = 0; sa < NS; ++sa) {
-                        const __nv_bfloat16* w = W + (sa * 2 * KB + tile * 16 + g) * P + k0 + 4 * t;
-                        const uint2 x = *reinterpret_cast<const uint2*>(w), y = *reinterpret_cast<const uint2*>(w + 8 * P);
-#pragma unroll
-                        for (int sb = 0; sb < NS - sa; ++sb)
-#pragma unroll
-                            for (int j = 0; j < VW; ++j) mma_16816(acc[i][j], x.x, y.x, x.y, y.y, b0[j][sb], b1[j][sb]);
-                    }
-                }
+        for (int e = 0; e < 16; ++e)
+            if (r0 + e < live && col < DV) v[e] = ((const T*)a.v)[(tok0 + (r0 + e) * a.H) * DV + col];
+    };
+    load_v(warp / 4 * 16, v0);
+    if (S0) {
+        fine = umma::block_wait(&sm.done, 0, a.err, kTreeErrBit);
+        umma::fence_after_sync();
+    }
+    if (fine && warp % 4 * 32 < DV)
+        for (int c0 = warp / 4 * 16; c0 < 2 * KP; c0 += 48) {
+            float x[16] = {};
+            if (S0) {
+                umma::tmem_ld16(sm.tmem + ((uint32_t)(warp % 4 * 32) << 16) + c0, x);
+                umma::tmem_wait_ld();
             }
-        __syncthreads();                                   // the rows are done with
+            if (c0 < KP) {                                 // keys: v - S0^T (..)
+                if (c0 >= 48) load_v(c0, v0);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int tile = rows + i * kRowGroups;
-            if (tile >= kTiles || tile % (KB / 16) * 16 >= live) continue;
+                for (int e = 0; e < 16; ++e)
+                    if (c0 + e < live) prod[(c0 + e) * DV + col] = IO<T>::load(v0, e) - x[e];
+            } else {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                Quad lo, hi;
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    lo.v[j] = acc[i][j][2 * half];
-                    hi.v[j] = acc[i][j][2 * half + 1];
-                }
-                float* to = prod + (tile * 16 + g + 8 * half) * DV + cols + 2 * VW * t;
-                *reinterpret_cast<Quad*>(to) = lo;
-                *reinterpret_cast<Quad*>(to + VW) = hi;
+                for (int e = 0; e < 16; ++e) prod[(KB + c0 - KP + e) * DV + col] = x[e];
             }
         }
-    } else {
-        for (int e = tid; e < 2 * KB * DV; e += 256) prod[e] = 0.f;
-    }
+    umma::fence_before_sync();
     __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 8) umma::tmem_dealloc(sm.tmem, kColumns);
+    if (!fine) return;
 
     // 4. level by level; a lane holds CPL columns
     constexpr int CPL = DV / 32;
     struct alignas(4 * CPL) Cols { float v[CPL]; };
-    // v of the warp's first node of a level is asked for one level before
-    const auto load_v = [&](int at) {
-        Cols v = {};
-        if (at < live) {
-            const T* p = (const T*)a.v + (tok0 + sm.order[at] * a.H) * DV + CPL * lane;
-            if constexpr (sizeof(T) == 4) {
-                v = *reinterpret_cast<const Cols*>(p);
-            } else {
-                struct alignas(2 * CPL) Raw { uint32_t u[CPL / 2]; };
-                const Raw r = *reinterpret_cast<const Raw*>(p);
-#pragma unroll
-                for (int e = 0; e < CPL; e += 2) {
-                    v.v[e] = __uint_as_float(r.u[e / 2] << 16);
-                    v.v[e + 1] = __uint_as_float(r.u[e / 2] & 0xffff0000u);
-                }
-            }
-        }
-        return v;
-    };
-    Cols ahead = load_v(warp);
     for (int done = 0, level = 1; done < live; ++level) {
         const int end = sm.level_end[level];
-        const Cols first = ahead;
-        ahead = load_v(end + warp);
-        for (int at = done + warp; at < end; at += 8) {
-            const Cols v = at == done + warp ? first : load_v(at);
+        for (int at = done + warp; at < end; at += kTreeThreads / 32) {
             const int i = sm.order[at], off = sm.off[i];
-            Cols pk = *reinterpret_cast<const Cols*>(prod + i * DV + CPL * lane);
+            Cols vk = *reinterpret_cast<const Cols*>(prod + i * DV + CPL * lane);
             Cols pq = *reinterpret_cast<const Cols*>(prod + (KB + i) * DV + CPL * lane);
             const int64_t to = (tok0 + i * a.H) * DV + CPL * lane;
 #pragma unroll 4
@@ -373,7 +384,7 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
                 const Cols u = *reinterpret_cast<const Cols*>(prod + sm.anc[off + p] * DV + CPL * lane);
 #pragma unroll
                 for (int e = 0; e < CPL; ++e) {
-                    pk.v[e] += ab.x * u.v[e];
+                    vk.v[e] -= ab.x * u.v[e];
                     pq.v[e] += ab.y * u.v[e];
                 }
             }
@@ -381,10 +392,10 @@ __global__ void __launch_bounds__(256, KB <= 32 ? 3 : 2) tree_fwd_kernel(TreeArg
             Cols o;
 #pragma unroll
             for (int e = 0; e < CPL; ++e) {
-                pk.v[e] = b * (v.v[e] - pk.v[e]);
-                o.v[e] = a.scale * (pq.v[e] + self * pk.v[e]);
+                vk.v[e] *= b;
+                o.v[e] = a.scale * (pq.v[e] + self * vk.v[e]);
             }
-            *reinterpret_cast<Cols*>(prod + i * DV + CPL * lane) = pk;
+            *reinterpret_cast<Cols*>(prod + i * DV + CPL * lane) = vk;
             if constexpr (sizeof(T) == 4) {
                 *reinterpret_cast<Cols*>((T*)a.out + to) = o;
             } else if constexpr (CPL == 4) {
@@ -471,14 +482,16 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(TreeArgs a)
 namespace {
 
 template <typename T, int DK, int DV, int KB>
-cudaError_t tree_fwd_kb(const TreeArgs& a, cudaStream_t st)
+cudaError_t tree_fwd_kb(TreeArgs a, cudaStream_t st)
 {
     constexpr int smem = (int)sizeof(TreeSmem<DK, DV, KB, sizeof(T) == 2 ? 2 : 3>);
     const cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T, DK, DV, KB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    constexpr int per_sm = KB <= 32 && sizeof(T) == 2 ? 2 : 1;
+    a.resident = device_sm_count() * per_sm;
     LaunchScope scope(st, K_TREE_FWD);
-    tree_fwd_kernel<T, DK, DV, KB><<<(unsigned)(a.N * a.H), 256, smem, st>>>(a);
+    tree_fwd_kernel<T, DK, DV, KB><<<(unsigned)(a.N * a.H), kTreeThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
