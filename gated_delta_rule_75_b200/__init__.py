@@ -153,6 +153,8 @@ def _ptr(t):
 
 
 def _check(t, name, dtype, shape, device):
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -427,6 +429,9 @@ def gdn_chunk_bwd(q, k, v, log_a, beta, scale, dout, h0=None, dhT=None, cu_seqle
                      need_dh0=need_dh0, _gdn=True)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's address, by device index
+
+
 def _call(name, dev, *args):
     """Calls a C entry point on ``dev``'s current stream, with ``dev`` current; tensors in
     ``args`` become their device addresses.  Raises KDAError on a failed status."""
@@ -434,11 +439,12 @@ def _call(name, dev, *args):
         raise ValueError(f"{name}: tensors must be on a CUDA device, not {dev}")
     fn = getattr(_lib or _load(), name)
     args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != KDA_OK:
         raise KDAError(st, name)
 

@@ -25,18 +25,20 @@ namespace kda {
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxD = 512;      // at most 16 elements a lane
 
-template <typename T, int VEC> struct Row;      // VEC consecutive elements, one access
+// VEC consecutive elements: one access, as they are stored (Raw) and as fp32.
+template <typename T, int VEC> struct Row;
 template <> struct Row<float, 4> {
-    static __device__ __forceinline__ void load(const float* p, float* v) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
+    using Raw = float4;
+    static __device__ __forceinline__ Raw load(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
+    static __device__ __forceinline__ void unpack(const Raw& x, float* v) {
         v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
     }
     static __device__ __forceinline__ void store(float* p, const float* v) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
     }
 };
-template <int VEC> struct RowBf16 {
-    static __device__ __forceinline__ void unpack(uint32_t u, float* v) {
+struct RowBf16 {
+    static __device__ __forceinline__ void two(uint32_t u, float* v) {
         v[0] = __uint_as_float(u << 16);
         v[1] = __uint_as_float(u & 0xffff0000u);
     }
@@ -45,28 +47,42 @@ template <int VEC> struct RowBf16 {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 };
-template <> struct Row<__nv_bfloat16, 8> : RowBf16<8> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* v) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        unpack(u.x, v); unpack(u.y, v + 2); unpack(u.z, v + 4); unpack(u.w, v + 6);
+template <> struct Row<__nv_bfloat16, 8> : RowBf16 {
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+    static __device__ __forceinline__ void unpack(const Raw& u, float* v) {
+        two(u.x, v); two(u.y, v + 2); two(u.z, v + 4); two(u.w, v + 6);
     }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack(v), pack(v + 2), pack(v + 4), pack(v + 6));
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack(v), pack(v + 2), pack(v + 4), pack(v + 6)));
     }
 };
-template <> struct Row<__nv_bfloat16, 4> : RowBf16<4> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* v) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        unpack(u.x, v); unpack(u.y, v + 2);
-    }
+template <> struct Row<__nv_bfloat16, 4> : RowBf16 {
+    using Raw = uint2;
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return __ldcs(reinterpret_cast<const uint2*>(p)); }
+    static __device__ __forceinline__ void unpack(const Raw& u, float* v) { two(u.x, v); two(u.y, v + 2); }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack(v), pack(v + 2));
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack(v), pack(v + 2)));
     }
 };
 template <typename T> struct Row<T, 1> {
-    static __device__ __forceinline__ void load(const T* p, float* v) { v[0] = IO<T>::load(p, 0); }
+    using Raw = T;
+    static __device__ __forceinline__ Raw load(const T* p) { return *p; }
+    static __device__ __forceinline__ void unpack(const Raw& x, float* v) { v[0] = IO<T>::load(&x, 0); }
     static __device__ __forceinline__ void store(T* p, const float* v) { IO<T>::store(p, 0, v[0]); }
 };
+
+// The lane's vectors of one row of a tensor; what lies past the row's end, or in no row, is zero.
+template <typename T, int VEC, int NV, int LPG>
+__device__ __forceinline__ void load_row(const T* row, bool on, int lane, int d, typename Row<T, VEC>::Raw (&r)[NV])
+{
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * LPG + lane) * VEC;
+        if (on && c < d) r[v] = Row<T, VEC>::load(row + c);
+        else r[v] = typename Row<T, VEC>::Raw{};
+    }
+}
 
 // Sum over the LPG lanes of a slot; every lane gets it.
 template <int LPG>
@@ -77,7 +93,18 @@ __device__ __forceinline__ float slot_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// fp32 I/O: within 3 half steps.  bf16 I/O: the exponential's argument is rounded once more and the
+// reciprocal is the hardware's, |z| + 4 half steps of 2^-24 together, far below the output's own 2^-8; it
+// takes 4 instructions for about 20, which is what bounded the kernel (65536 x 32 x 128: 411 -> 2xx us).
+template <typename T> __device__ __forceinline__ float sigmoid(float z);
+template <> __device__ __forceinline__ float sigmoid<float>(float z) { return 1.f / (1.f + expf(-z)); }
+template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float z)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 // Which rows a slot takes.
 struct SlotPlan {
@@ -109,22 +136,24 @@ group_norm_fwd_kernel(const T* __restrict__ x, const T* __restrict__ gate,
             w[v][e] = in && weight ? weight[(per_group ? g * p.d : 0) + c] : 1.f;
             b[v][e] = in && bias ? bias[(per_group ? g * p.d : 0) + c] : 0.f;
         }
-    // every lane of a warp makes the same number of rounds (the shuffles need all of them)
-    for (int64_t m = used ? slot / p.G : p.M; __any_sync(0xffffffffu, m < p.M); m += p.stride) {
+    // every lane of a warp makes the same number of rounds (the shuffles need all of them); the next
+    // row is on its way while this one is worked on
+    typename Row<T, VEC>::Raw next_x[NV], next_z[NV] = {};
+    int64_t m = used ? slot / p.G : p.M, at = (m * p.G + g) * p.d;
+    const int64_t pitch = p.stride * p.G * p.d;
+    load_row<T, VEC, NV, LPG>(x + at, m < p.M, lane, p.d, next_x);
+    if (gate) load_row<T, VEC, NV, LPG>(gate + at, m < p.M, lane, p.d, next_z);
+    for (; __any_sync(0xffffffffu, m < p.M); m += p.stride, at += pitch) {
         const bool on = m < p.M;
-        const int64_t at = (m * p.G + g) * p.d;
         float r[NV][VEC], z[NV][VEC];
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * LPG + lane) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) r[v][e] = 0.f, z[v][e] = 0.f;
-            if (on && c < p.d) {
-                Row<T, VEC>::load(x + at + c, r[v]);
-                if (gate) Row<T, VEC>::load(gate + at + c, z[v]);
-            }
+            Row<T, VEC>::unpack(next_x[v], r[v]);
+            Row<T, VEC>::unpack(next_z[v], z[v]);
         }
+        load_row<T, VEC, NV, LPG>(x + at + pitch, m + p.stride < p.M, lane, p.d, next_x);
+        if (gate) load_row<T, VEC, NV, LPG>(gate + at + pitch, m + p.stride < p.M, lane, p.d, next_z);
         if (center) {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
@@ -146,12 +175,16 @@ group_norm_fwd_kernel(const T* __restrict__ x, const T* __restrict__ gate,
         for (int v = 0; v < NV; ++v) {
             const int c = (v * LPG + lane) * VEC;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float n = r[v][e] * rstd * w[v][e] + b[v][e];
-                const float t = gate ? z[v][e] : n;
-                const float f = act == KDA_ACT_NONE ? t : act == KDA_ACT_SIGMOID ? sigmoid(t) : t * sigmoid(t);
-                r[v][e] = gate ? n * f : f;
-            }
+            for (int e = 0; e < VEC; ++e) r[v][e] = r[v][e] * rstd * w[v][e] + b[v][e];
+            if (act != KDA_ACT_NONE)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float t = gate ? z[v][e] : r[v][e], s = sigmoid<T>(t);
+                    z[v][e] = act == KDA_ACT_SILU ? t * s : s;
+                }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                r[v][e] = gate ? r[v][e] * z[v][e] : act != KDA_ACT_NONE ? z[v][e] : r[v][e];
             if (on && c < p.d) Row<T, VEC>::store(out + at + c, r[v]);
         }
     }
@@ -183,21 +216,25 @@ group_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ gate,
             dw[v][e] = 0.f;
             db[v][e] = 0.f;
         }
-    for (int64_t m = used ? slot / p.G : p.M; __any_sync(0xffffffffu, m < p.M); m += p.stride) {
+    typename Row<T, VEC>::Raw next_x[NV], next_z[NV] = {}, next_y[NV];
+    int64_t m = used ? slot / p.G : p.M, at = (m * p.G + g) * p.d;
+    const int64_t pitch = p.stride * p.G * p.d;
+    const auto fetch = [&](int64_t from, bool on) {
+        load_row<T, VEC, NV, LPG>(x + from, on, lane, p.d, next_x);
+        if (gate) load_row<T, VEC, NV, LPG>(gate + from, on, lane, p.d, next_z);
+        load_row<T, VEC, NV, LPG>(dout + from, on, lane, p.d, next_y);
+    };
+    fetch(at, m < p.M);
+    for (; __any_sync(0xffffffffu, m < p.M); m += p.stride, at += pitch) {
         const bool on = m < p.M;
-        const int64_t at = (m * p.G + g) * p.d;
         float r[NV][VEC], z[NV][VEC], y[NV][VEC];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * LPG + lane) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) r[v][e] = 0.f, z[v][e] = 0.f, y[v][e] = 0.f;
-            if (on && c < p.d) {
-                Row<T, VEC>::load(x + at + c, r[v]);
-                if (gate) Row<T, VEC>::load(gate + at + c, z[v]);
-                Row<T, VEC>::load(dout + at + c, y[v]);
-            }
+            Row<T, VEC>::unpack(next_x[v], r[v]);
+            Row<T, VEC>::unpack(next_z[v], z[v]);
+            Row<T, VEC>::unpack(next_y[v], y[v]);
         }
+        fetch(at + pitch, m + p.stride < p.M);
         if (center) {
             float sum = 0.f;
 #pragma unroll
@@ -225,9 +262,9 @@ group_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ gate,
                 const float t = gate ? z[v][e] : n;
                 float f = t, df = 1.f;
                 if (act != KDA_ACT_NONE) {
-                    const float s = sigmoid(t);
-                    f = act == KDA_ACT_SIGMOID ? s : t * s;
-                    df = act == KDA_ACT_SIGMOID ? s * (1.f - s) : s * (1.f + t * (1.f - s));
+                    const float s = sigmoid<T>(t);
+                    f = act == KDA_ACT_SILU ? t * s : s;
+                    df = s + (act == KDA_ACT_SILU ? f : -s) * (act == KDA_ACT_SILU ? 1.f - s : s);
                 }
                 const float dn = y[v][e] * (gate ? f : df);
                 z[v][e] = y[v][e] * n * df;      // dgate
@@ -313,7 +350,16 @@ group_norm_wgrad_kernel(const float* __restrict__ wpart, const float* __restrict
 
 namespace {
 
-SlotPlan plan_slots(const GroupNormArgs& a, int lpg, int ctas_most, int& grid)
+// CTAs of the kernel that an SM holds at once: the grid is one wave of them, so that all slots work from
+// the first row to the last.
+template <typename Kernel> int64_t resident(Kernel kernel)
+{
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNormThreads, 0) != cudaSuccess || n < 1) n = 1;
+    return n * device_sm_count();
+}
+
+SlotPlan plan_slots(const GroupNormArgs& a, int lpg, int64_t ctas_most, int& grid)
 {
     const int64_t room = kNormThreads / lpg;
     SlotPlan p;
@@ -334,7 +380,8 @@ template <typename T, int VEC, int NV, int LPG>
 cudaError_t norm_fwd(const GroupNormArgs& a, cudaStream_t st)
 {
     int grid;
-    const SlotPlan p = plan_slots(a, LPG, 148 * 8, grid);
+    static const int64_t most = resident(group_norm_fwd_kernel<T, VEC, NV, LPG>);
+    const SlotPlan p = plan_slots(a, LPG, most, grid);
     LaunchScope scope(st, K_GNORM_FWD);
     group_norm_fwd_kernel<T, VEC, NV, LPG><<<grid, kNormThreads, 0, st>>>(
         (const T*)a.x, (const T*)a.gate, a.weight, a.bias, (T*)a.out, p, a.per_group, a.center, a.eps, a.act);
@@ -345,7 +392,8 @@ template <typename T, int VEC, int NV, int LPG>
 cudaError_t norm_bwd(const GroupNormArgs& a, cudaStream_t st)
 {
     int grid;
-    const SlotPlan p = plan_slots(a, LPG, 148 * 4, grid);
+    static const int64_t most = resident(group_norm_bwd_kernel<T, VEC, NV, LPG>);
+    const SlotPlan p = plan_slots(a, LPG, most, grid);
     const int64_t heads = a.per_group ? a.G : 1;
     const int64_t rows = heads <= p.per_cta ? grid : p.slots / a.G, cols = heads * a.d;
     StreamBuffer buf;
@@ -371,15 +419,14 @@ cudaError_t norm_bwd(const GroupNormArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// F(LPG, NV) for rows of `vecs` vectors.
+// F(NV, LPG) for rows of `vecs` vectors of VEC elements.
 #define KDA_NORM_BY_VECS(F, T, VEC)                                             \
     do {                                                                       \
-        if (vecs <= 4) return F<T, VEC, 1, 4>(a, st);                           \
         if (vecs <= 8) return F<T, VEC, 1, 8>(a, st);                           \
         if (vecs <= 16) return F<T, VEC, 1, 16>(a, st);                         \
         if (vecs <= 32) return F<T, VEC, 1, 32>(a, st);                         \
-        if (vecs <= 64) return F<T, VEC, 2, 32>(a, st);                         \
-        return F<T, VEC, 4, 32>(a, st);                                        \
+        if (VEC == 8 || vecs <= 64) return F<T, VEC, 2, 32>(a, st);             \
+        return F<T, VEC, VEC == 8 ? 2 : 4, 32>(a, st);                          \
     } while (0)
 // ceil(d / 32) elements a lane, for widths that no vector divides
 #define KDA_NORM_SCALAR(F, T)                                                   \
