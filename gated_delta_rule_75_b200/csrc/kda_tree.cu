@@ -410,73 +410,88 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
 }
 
 // The accepted path's tokens applied to the cached state, in place: the decode step's
-// arithmetic once per token, with the state in registers from the first to the last.
-// One CTA of 256 threads for one (sequence, head).
+// arithmetic once per token, with the state in registers from the first to the last, so that
+// it is read and written once however long the path (bound by memory: 128 KiB a head at
+// d = 128).  One CTA of 256 threads for kCommitCols columns of one (sequence, head): columns
+// go their own way, and more, smaller CTAs on an SM mix loads, arithmetic and stores better.
+// The tokens of up to kCommitAhead places of the path are brought in together, while the state
+// is on its way.
+constexpr int kCommitAhead = 8, kCommitCols = 64;
+
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(256) tree_commit_kernel(TreeArgs a)
+__global__ void __launch_bounds__(256, 4) tree_commit_kernel(const TreeArgs a)
 {
-    constexpr int TPR = DV / 4;        // threads per state row (float4 each)
+    constexpr int DB = kCommitCols, TPR = DB / 4;      // columns; threads per state row (float4 each)
     constexpr int RG = 256 / TPR;      // row groups
     constexpr int RPT = DK / RG;       // rows per thread
-    __shared__ float sk[DK], sa[DK], sv[DV], se[DV];
+    __shared__ float sk[kCommitAhead][DK], sa[kCommitAhead][DK], sv[kCommitAhead][DB], se[DB], sb[kCommitAhead];
     __shared__ float4 red[RG][TPR];
-    __shared__ int path[64];           // accepted node first
+    __shared__ int par[KDA_TREE_MAX_NODES], path[KDA_TREE_MAX_NODES];   // accepted node first
     __shared__ int count;
     const int tid = threadIdx.x, c4 = tid % TPR, rg = tid / TPR;
-    const int64_t n = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int64_t item = blockIdx.x / (DV / DB), n = item / a.H, h = item % a.H;
+    const int c0 = (int)(blockIdx.x % (DV / DB)) * DB;
     const int K = (int)a.K;
     const int64_t sl = a.slots ? a.slots[n] : n;
     const int last = a.accepted[n];
+    if (tid < K) par[tid] = a.parents[n * K + tid];
     if (sl >= a.P || last >= K || last < -1) {
         if (tid == 0) atomicOr(a.err, kErrSeqlens);
         return;
     }
     if (sl < 0 || last < 0) return;
-    float4* S4 = reinterpret_cast<float4*>(a.state + (sl * a.H + h) * (int64_t)DK * DV);
+    float4* S4 = reinterpret_cast<float4*>(a.state + (sl * a.H + h) * (int64_t)DK * DV + c0);
     float4 s[RPT];
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) s[r] = __ldcs(&S4[(rg * RPT + r) * TPR + c4]);
+    for (int r = 0; r < RPT; ++r) s[r] = __ldcs(&S4[(rg * RPT + r) * (DV / 4) + c4]);
+    __syncthreads();
     if (tid == 0) {
         int c = 0;
-        for (int i = last; i >= 0; i = tree_parent(a.parents + n * K, i, a.err)) path[c++] = i;
+        for (int i = last; i >= 0; i = tree_parent(par, i, a.err)) path[c++] = i;
         count = c;
     }
     __syncthreads();
-    for (int p = count - 1; p >= 0; --p) {
-        const int64_t tok = (n * K + path[p]) * a.H + h;
-        for (int i = tid; i < DK; i += 256) {
-            sk[i] = IO<T>::load((const T*)a.k, tok * DK + i);
-            sa[i] = expf(a.log_alpha[tok * DK + i]);
+    for (int left = count; left > 0; left -= kCommitAhead) {
+        const int now = left < kCommitAhead ? left : kCommitAhead;
+        for (int e = tid; e < now * DK; e += 256) {
+            const int64_t tok = (n * K + path[left - 1 - e / DK]) * a.H + h;
+            sk[e / DK][e % DK] = IO<T>::load((const T*)a.k, tok * DK + e % DK);
+            sa[e / DK][e % DK] = expf(__ldcs(a.log_alpha + tok * DK + e % DK));
         }
-        for (int j = tid; j < DV; j += 256) sv[j] = IO<T>::load((const T*)a.v, tok * DV + j);
-        const float b = a.beta[tok];
+        for (int e = tid; e < now * DB; e += 256) {
+            const int64_t tok = (n * K + path[left - 1 - e / DB]) * a.H + h;
+            sv[e / DB][e % DB] = IO<T>::load((const T*)a.v, tok * DV + c0 + e % DB);
+        }
+        if (tid < now) sb[tid] = a.beta[(n * K + path[left - 1 - tid]) * a.H + h];
         __syncthreads();
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < now; ++p) {
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-            const float al = sa[rg * RPT + r], kk = sk[rg * RPT + r];
-            s[r].x *= al; s[r].y *= al; s[r].z *= al; s[r].w *= al;
-            acc.x += kk * s[r].x; acc.y += kk * s[r].y; acc.z += kk * s[r].z; acc.w += kk * s[r].w;
-        }
-        red[rg][c4] = acc;
-        __syncthreads();
-        for (int j = tid; j < DV; j += 256) {
-            float vh = 0.f;
+            for (int r = 0; r < RPT; ++r) {
+                const float al = sa[p][rg * RPT + r], kk = sk[p][rg * RPT + r];
+                s[r].x *= al; s[r].y *= al; s[r].z *= al; s[r].w *= al;
+                acc.x += kk * s[r].x; acc.y += kk * s[r].y; acc.z += kk * s[r].z; acc.w += kk * s[r].w;
+            }
+            red[rg][c4] = acc;
+            __syncthreads();
+            for (int j = tid; j < DB; j += 256) {
+                float vh = 0.f;
 #pragma unroll
-            for (int g = 0; g < RG; ++g) vh += reinterpret_cast<const float*>(&red[g][0])[j];
-            se[j] = b * (sv[j] - vh);
-        }
-        __syncthreads();
-        const float4 e = reinterpret_cast<const float4*>(se)[c4];
+                for (int g = 0; g < RG; ++g) vh += reinterpret_cast<const float*>(&red[g][0])[j];
+                se[j] = sb[p] * (sv[p][j] - vh);
+            }
+            __syncthreads();
+            const float4 e = reinterpret_cast<const float4*>(se)[c4];
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-            const float kk = sk[rg * RPT + r];
-            s[r].x += kk * e.x; s[r].y += kk * e.y; s[r].z += kk * e.z; s[r].w += kk * e.w;
+            for (int r = 0; r < RPT; ++r) {
+                const float kk = sk[p][rg * RPT + r];
+                s[r].x += kk * e.x; s[r].y += kk * e.y; s[r].z += kk * e.z; s[r].w += kk * e.w;
+            }
         }
-        __syncthreads();
+        __syncthreads();               // the tokens' places are filled again
     }
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) __stcs(&S4[(rg * RPT + r) * TPR + c4], s[r]);
+    for (int r = 0; r < RPT; ++r) __stcs(&S4[(rg * RPT + r) * (DV / 4) + c4], s[r]);
 }
 
 namespace {
@@ -507,8 +522,9 @@ cudaError_t tree_fwd_t(const TreeArgs& a, cudaStream_t st)
 template <typename T, int DK, int DV>
 cudaError_t tree_commit_t(const TreeArgs& a, cudaStream_t st)
 {
+
     LaunchScope scope(st, K_TREE_COMMIT);
-    tree_commit_kernel<T, DK, DV><<<(unsigned)(a.N * a.H), 256, 0, st>>>(a);
+    tree_commit_kernel<T, DK, DV><<<(unsigned)(a.N * a.H * (DV / kCommitCols)), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -549,7 +565,7 @@ kda_status_t tree_check(int64_t N, int64_t P, int64_t K, int64_t H, int64_t dk, 
     if (N < 0 || P < 0 || K < 0 || H < 0) return KDA_ERR_INVALID_ARG;
     if (io != KDA_IO_F32 && io != KDA_IO_BF16) return KDA_ERR_UNSUPPORTED;
     if (!tree_dim_ok(dk) || !tree_dim_ok(dv) || K > KDA_TREE_MAX_NODES) return KDA_ERR_UNSUPPORTED;
-    if (N > 0x7fffffffLL || H > 0x7fffffffLL || N * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (N > 0x7fffffffLL || H > 0x7fffffffLL || N * H > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
     if (H > 0 && P > (int64_t(1) << 40) / H) return KDA_ERR_UNSUPPORTED;
     *empty = N == 0 || H == 0 || K == 0;
     return KDA_OK;
