@@ -64,19 +64,25 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&s)[NS])
     }
 }
 
-constexpr int kTreeThreads = 384, kTreeWalkers = 256;
+// Eight lanes for every node walk; four more warps bring S0.
+constexpr int tree_walkers(int KB) { return 8 * KB; }
+constexpr int kTreeStagers = 128;
+// CTAs of an SM, by their registers and shared memory.
+constexpr int tree_per_sm(int KB, int io_bytes) { return KB == 64 ? 1 : KB == 32 ? (io_bytes == 2 ? 2 : 1) : (io_bytes == 2 ? 3 : 2); }
 constexpr int kTreeErrBit = 2;                             // "operand MMAs" of the error word
 
 // Shared memory of a CTA for trees of up to KB nodes.
 template <int DK, int DV, int KB, int NS>
 struct TreeSmem {
     static constexpr int kPairs = KB * (KB + 1) / 2;
-    static constexpr int kState = DK * DV * 2;             // bytes of one summand of S0
+    // S0 comes in one piece, or, where that lets a third CTA onto the SM, 64 rows at a time
+    static constexpr int kPieces = KB == 16 ? DK / 64 : 1, kRows = DK / kPieces;
+    static constexpr int kState = kRows * DV * 2;          // bytes of one summand of a piece
     // with dv = 64 the upper half of the M = 128 operand is whatever follows: its rows are not used
-    static constexpr int kSlack = DV == 64 ? DK * 128 : 0;
+    static constexpr int kSlack = DV == 64 ? kRows * 128 : 0;
     static constexpr int kA = 2 * KB * DK * 4, kB = NS * 2 * KB * DK * 2, kC = 2 * KB * DV * 4;
     static constexpr int kRegion = kA > kB ? (kA > kC ? kA : kC) : (kB > kC ? kB : kC);
-    // S0: [NS] of blocks of 64 columns, [DK][64] bf16 each, 128-byte swizzle (M-major operand)
+    // S0: [NS] of blocks of 64 columns, [kRows][64] bf16 each, 128-byte swizzle (M-major operand)
     alignas(1024) unsigned char state[NS * kState + kSlack];
     // alpha, k [KB][DK]; then the rows, [NS] of blocks of 64 channels, [2 KP][64] bf16 each, 128-byte
     // swizzle (K-major operand); then the products with S0 [2][KB][DV], whose first half becomes u
@@ -84,7 +90,7 @@ struct TreeSmem {
     float2 ab[kPairs];                                     // A, B of a node, by place on its path, itself at 0
     float beta[KB];
     int par[KB], depth[KB], off[KB], order[KB], level_end[KB + 1];
-    uint64_t done;                                         // the product
+    uint64_t done[kPieces];                                // the products
     uint32_t tmem;
     unsigned char anc[kPairs];                             // the node at that place
 };
@@ -109,16 +115,20 @@ __device__ __forceinline__ void prefetch_item(const TreeArgs& a, int64_t n, int6
     prefetch_l2<DV * sizeof(T)>((const T*)a.v + tok * DV);
 }
 
-// Warps 0 - 7 only.
-__device__ __forceinline__ void walkers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTreeWalkers) : "memory"); }
+// The walking warps, the staging warps.
+template <int KB> __device__ __forceinline__ void walkers_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(tree_walkers(KB)) : "memory");
+}
+__device__ __forceinline__ void stagers_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kTreeStagers) : "memory"); }
 
 template <typename T, int DK, int DV, int KB>
-__global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 : 1) tree_fwd_kernel(const TreeArgs a)
+__global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(KB, sizeof(T))) tree_fwd_kernel(const TreeArgs a)
 {
     constexpr int NS = sizeof(T) == 2 ? 2 : 3;
     using Smem = TreeSmem<DK, DV, KB, NS>;
     constexpr int kQuads = DK / 32;                        // float4 channel groups of a lane in the walk
-    constexpr int kPerGroup = (KB + 31) / 32;              // nodes of a group of eight lanes
+    constexpr int kWalkers = tree_walkers(KB), kThreads = kWalkers + kTreeStagers, kStageWarp = kWalkers / 32;
     constexpr int kColumns = 2 * KB < 32 ? 32 : 2 * KB;    // of tensor memory
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
@@ -143,36 +153,57 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
     if (live == 0) return;
     const int64_t tok0 = (n * K) * a.H + h;                // node i: tok0 + i * H
     const int KP = (live + 15) / 16 * 16;                  // rows of keys, and of queries
-    if (warp == 8) {
+    if (warp == kStageWarp) {
         umma::tmem_alloc(&sm.tmem, kColumns);
         umma::tmem_relinquish();
     }
     if (tid == 0) {
-        umma::mbar_init(&sm.done, 1);
+        for (int i = 0; i < Smem::kPieces; ++i) umma::mbar_init(&sm.done[i], 1);
         umma::fence_mbar_init();
     }
     float* prod = reinterpret_cast<float*>(sm.region);
-    if (warp >= 8) {
-        // S0: a row (two rows of 64 columns) a warp at a time
-        constexpr int kLoads = 8, kPerRow = DV / 4, kStep = (kTreeThreads - kTreeWalkers) / kPerRow;
-        const int mine = tid - kTreeWalkers, c = mine % kPerRow * 4, r0 = mine / kPerRow;
-        if (S0)
-            for (int k0 = r0; k0 < DK; k0 += kLoads * kStep) {
-                float4 s[kLoads];
+    // S0, by the staging warps: a row (two rows of 64 columns) a warp at a time
+    constexpr int kPerRow = DV / 4, kStep = kTreeStagers / kPerRow, kLoads = 8;
+    const int mine = tid - kWalkers, sc = mine % kPerRow * 4, sr = mine / kPerRow;
+    const auto stage = [&](int piece) {
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    s[i] = __ldcs(reinterpret_cast<const float4*>(S0 + (k0 + i * kStep) * DV + c));
+        for (int k0 = 0; k0 < Smem::kRows; k0 += kLoads * kStep) {
+            float4 s[kLoads];
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    uint32_t lo[NS], hi[NS];
-                    split<NS>(s[i].x, s[i].y, lo);
-                    split<NS>(s[i].z, s[i].w, hi);
-                    const uint32_t to = c / 64 * (DK * 128) + umma::sw128_offset(k0 + i * kStep, c % 64);
+            for (int i = 0; i < kLoads; ++i)
+                s[i] = __ldcs(reinterpret_cast<const float4*>(S0 + (piece * Smem::kRows + k0 + sr + i * kStep) * DV + sc));
+            if (piece > 0 && k0 == 0) umma::mbar_wait(&sm.done[piece - 1], 0, a.err, kTreeErrBit);
 #pragma unroll
-                    for (int e = 0; e < NS; ++e)
-                        *reinterpret_cast<uint2*>(sm.state + e * Smem::kState + to) = make_uint2(lo[e], hi[e]);
-                }
+            for (int i = 0; i < kLoads; ++i) {
+                uint32_t lo[NS], hi[NS];
+                split<NS>(s[i].x, s[i].y, lo);
+                split<NS>(s[i].z, s[i].w, hi);
+                const uint32_t to = sc / 64 * (Smem::kRows * 128) + umma::sw128_offset(k0 + sr + i * kStep, sc % 64);
+#pragma unroll
+                for (int e = 0; e < NS; ++e)
+                    *reinterpret_cast<uint2*>(sm.state + e * Smem::kState + to) = make_uint2(lo[e], hi[e]);
             }
+        }
+    };
+    // the products with one piece, by one thread
+    const auto multiply = [&](int piece) {
+        const uint32_t idesc = umma::make_idesc_bf16(128, 2 * KP, true, false);
+        const uint64_t ad = umma::make_desc(umma::smem_u32(sm.state), Smem::kRows * 128, 1024);
+        const uint64_t bd = umma::make_desc(umma::smem_u32(sm.region), 16, 1024);
+        const uint32_t block = 2 * KP * 128 / 16;          // of the rows' channels, in descriptor units
+#pragma unroll
+        for (int sa = 0; sa < NS; ++sa)                    // summand of S0, of the rows
+#pragma unroll
+            for (int sb = 0; sb < NS - sa; ++sb)
+#pragma unroll
+                for (int ks = 0; ks < Smem::kRows / 16; ++ks)
+                    umma::mma_bf16(sm.tmem, ad + (sa * Smem::kState + ks * 2048) / 16,
+                                   bd + (sb * (DK / 64) + piece * (Smem::kRows / 64) + ks / 4) * block + ks % 4 * 2, idesc,
+                                   piece + sa + sb + ks > 0);
+        umma::commit(&sm.done[piece]);
+    };
+    if (warp >= kStageWarp) {
+        if (S0) stage(0);
         // what the CTA that follows this one on the SM will read goes into the L2 meanwhile, or memory
         // would idle while this one computes
         const int64_t next = (int64_t)blockIdx.x + a.resident;
@@ -190,12 +221,12 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
                 asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.v + (tok0 + tid * a.H) * DV * sizeof(T) + c));
         }
         if (tid <= KB) sm.level_end[tid] = 0;
-        constexpr int kAhead = KB >= 32 ? 4 : 2;               // quads of alpha and k a thread has on their way
-        for (int e0 = tid; e0 < live * (DK / 4); e0 += kTreeWalkers * kAhead) {
+        constexpr int kAhead = 4;                              // quads of alpha and k a thread has on their way
+        for (int e0 = tid; e0 < live * (DK / 4); e0 += kWalkers * kAhead) {
             float4 g[kAhead], k[kAhead];
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
-                const int e = e0 + r * kTreeWalkers, i = e / (DK / 4), c = e % (DK / 4) * 4;
+                const int e = e0 + r * kWalkers, i = e / (DK / 4), c = e % (DK / 4) * 4;
                 if (e >= live * (DK / 4)) break;
                 const int64_t at = (tok0 + i * a.H) * DK + c;
                 g[r] = __ldcs(reinterpret_cast<const float4*>(a.log_alpha + at));
@@ -203,19 +234,19 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
             }
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
-                const int e = e0 + r * kTreeWalkers;
+                const int e = e0 + r * kWalkers;
                 if (e >= live * (DK / 4)) break;
                 *reinterpret_cast<float4*>(alpha + 4 * e) = make_float4(expf(g[r].x), expf(g[r].y), expf(g[r].z), expf(g[r].w));
                 *reinterpret_cast<float4*>(kf + 4 * e) = k[r];
             }
         }
-        walkers_sync();
+        walkers_sync<KB>();
         if (tid < live) {
             int d = 1;                                         // nodes on the path, itself too
             for (int j = sm.par[tid]; j >= 0; j = sm.par[j]) ++d;
             sm.depth[tid] = d;
         }
-        walkers_sync();
+        walkers_sync<KB>();
         if (tid < live) {
             const int mine = sm.depth[tid];
             int off = 0, pos = 0;
@@ -228,17 +259,14 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
             sm.order[pos] = tid;
             atomicMax(&sm.level_end[mine], pos + 1);
         }
-        walkers_sync();
+        walkers_sync<KB>();
 
         // 2. the walks: lane l of a group holds channels 4 (l + 8 m) .. + 3
         const int l8 = lane % 8;
-        float4 wk[kPerGroup][kQuads], wq[kPerGroup][kQuads];
-        int node[kPerGroup];
-#pragma unroll
-        for (int r = 0; r < kPerGroup; ++r) {
-            const int at = r * 32 + warp * 4 + lane / 8;
-            const int i = at < live ? sm.order[at] : -1;
-            node[r] = i;
+        float4 wk[kQuads], wq[kQuads];
+        const int node = warp * 4 + lane / 8 < live ? sm.order[warp * 4 + lane / 8] : -1;
+        {
+            const int i = node;
             int j = -1, place = 0;
             float2 dot = make_float2(0.f, 0.f);
             if (i >= 0) {
@@ -251,8 +279,8 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
                     const float4 k = *reinterpret_cast<const float4*>(kf + i * DK + c);
                     const float4 g = *reinterpret_cast<const float4*>(alpha + i * DK + c);
                     dot.y += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-                    wk[r][m] = make_float4(k.x * g.x, k.y * g.y, k.z * g.z, k.w * g.w);
-                    wq[r][m] = make_float4(q.x * g.x, q.y * g.y, q.z * g.z, q.w * g.w);
+                    wk[m] = make_float4(k.x * g.x, k.y * g.y, k.z * g.z, k.w * g.w);
+                    wq[m] = make_float4(q.x * g.x, q.y * g.y, q.z * g.z, q.w * g.w);
                 }
             }
             int at_node = i;                                   // the node whose dots are in `dot`
@@ -276,7 +304,7 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
                         const int c = 4 * (l8 + 8 * m);
                         const float4 k = *reinterpret_cast<const float4*>(kf + j * DK + c);
                         const float4 g = *reinterpret_cast<const float4*>(alpha + j * DK + c);
-                        float4 &x = wk[r][m], &y = wq[r][m];
+                        float4 &x = wk[m], &y = wq[m];
                         dot.x += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
                         dot.y += y.x * k.x + y.y * k.y + y.z * k.z + y.w * k.w;
                         x.x *= g.x; x.y *= g.y; x.z *= g.z; x.w *= g.w;
@@ -286,23 +314,21 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
                 }
             }
         }
-        walkers_sync();                                        // alpha and k are done with
+        walkers_sync<KB>();                                        // alpha and k are done with
 
         // 3. the rows
         if (S0) {
-#pragma unroll
-            for (int r = 0; r < kPerGroup; ++r)
-                if (node[r] >= 0)
+            if (node >= 0)
 #pragma unroll
                     for (int m = 0; m < kQuads; ++m)
 #pragma unroll
                         for (int which = 0; which < 2; ++which) {
-                            const float4 x = which ? wq[r][m] : wk[r][m];
+                            const float4 x = which ? wq[m] : wk[m];
                             uint32_t lo[NS], hi[NS];
                             split<NS>(x.x, x.y, lo);
                             split<NS>(x.z, x.w, hi);
                             const int c = 4 * (l8 + 8 * m);
-                            const uint32_t to = c / 64 * (2 * KP * 128) + umma::sw128_offset(which * KP + node[r], c % 64);
+                            const uint32_t to = c / 64 * (2 * KP * 128) + umma::sw128_offset(which * KP + node, c % 64);
 #pragma unroll
                             for (int e = 0; e < NS; ++e)
                                 *reinterpret_cast<uint2*>(sm.region + e * (2 * KP * DK * 2) + to) = make_uint2(lo[e], hi[e]);
@@ -315,20 +341,12 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
     umma::fence_after_sync();
     bool fine = true;
     if (S0) {
-        if (tid == 0) {
-            const uint32_t idesc = umma::make_idesc_bf16(128, 2 * KP, true, false);
-            const uint64_t ad = umma::make_desc(umma::smem_u32(sm.state), DK * 128, 1024);
-            const uint64_t bd = umma::make_desc(umma::smem_u32(sm.region), 16, 1024);
-            const uint32_t block = 2 * KP * 128 / 16;      // of the rows' channels, in descriptor units
-#pragma unroll
-            for (int sa = 0; sa < NS; ++sa)                // summand of S0, of the rows
-#pragma unroll
-                for (int sb = 0; sb < NS - sa; ++sb)
-#pragma unroll
-                    for (int ks = 0; ks < DK / 16; ++ks)
-                        umma::mma_bf16(sm.tmem, ad + (sa * Smem::kState + ks * 2048) / 16,
-                                       bd + (sb * (DK / 64) + ks / 4) * block + ks % 4 * 2, idesc, sa + sb + ks > 0);
-            umma::commit(&sm.done);
+        if (tid == 0) multiply(0);
+        if (Smem::kPieces > 1 && warp >= kStageWarp) {
+            stage(1);
+            umma::fence_smem_to_async();
+            stagers_sync();
+            if (tid == kWalkers) multiply(1);
         }
     }
     // a thread's column and its first 16 rows: v is asked for before the wait.  Lane = column of S0,
@@ -342,18 +360,18 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
     };
     load_v(warp / 4 * 16, v0);
     if (S0) {
-        fine = umma::block_wait(&sm.done, 0, a.err, kTreeErrBit);
+        fine = umma::block_wait(&sm.done[Smem::kPieces - 1], 0, a.err, kTreeErrBit);
         umma::fence_after_sync();
     }
     if (fine && warp % 4 * 32 < DV)
-        for (int c0 = warp / 4 * 16; c0 < 2 * KP; c0 += 48) {
+        for (int c0 = warp / 4 * 16; c0 < 2 * KP; c0 += kThreads / 128 * 16) {
             float x[16] = {};
             if (S0) {
                 umma::tmem_ld16(sm.tmem + ((uint32_t)(warp % 4 * 32) << 16) + c0, x);
                 umma::tmem_wait_ld();
             }
             if (c0 < KP) {                                 // keys: v - S0^T (..)
-                if (c0 >= 48) load_v(c0, v0);
+                if (c0 >= kThreads / 128 * 16) load_v(c0, v0);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (c0 + e < live) prod[(c0 + e) * DV + col] = IO<T>::load(v0, e) - x[e];
@@ -365,7 +383,7 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    if (warp == 8) umma::tmem_dealloc(sm.tmem, kColumns);
+    if (warp == kStageWarp) umma::tmem_dealloc(sm.tmem, kColumns);
     if (!fine) return;
 
     // 4. level by level; a lane holds CPL columns
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(kTreeThreads, KB <= 32 && sizeof(T) == 2 ? 2 :
     struct alignas(4 * CPL) Cols { float v[CPL]; };
     for (int done = 0, level = 1; done < live; ++level) {
         const int end = sm.level_end[level];
-        for (int at = done + warp; at < end; at += kTreeThreads / 32) {
+        for (int at = done + warp; at < end; at += kThreads / 32) {
             const int i = sm.order[at], off = sm.off[i];
             Cols vk = *reinterpret_cast<const Cols*>(prod + i * DV + CPL * lane);
             Cols pq = *reinterpret_cast<const Cols*>(prod + (KB + i) * DV + CPL * lane);
@@ -503,10 +521,9 @@ cudaError_t tree_fwd_kb(TreeArgs a, cudaStream_t st)
     const cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T, DK, DV, KB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    constexpr int per_sm = KB <= 32 && sizeof(T) == 2 ? 2 : 1;
-    a.resident = device_sm_count() * per_sm;
+    a.resident = device_sm_count() * tree_per_sm(KB, sizeof(T));
     LaunchScope scope(st, K_TREE_FWD);
-    tree_fwd_kernel<T, DK, DV, KB><<<(unsigned)(a.N * a.H), kTreeThreads, smem, st>>>(a);
+    tree_fwd_kernel<T, DK, DV, KB><<<(unsigned)(a.N * a.H), tree_walkers(KB) + kTreeStagers, smem, st>>>(a);
     return cudaGetLastError();
 }
 
