@@ -163,26 +163,26 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
     }
     float* prod = reinterpret_cast<float*>(sm.region);
     // S0, by the staging warps: a row (two rows of 64 columns) a warp at a time
-    constexpr int kPerRow = DV / 4, kStep = kTreeStagers / kPerRow, kLoads = 8;
+    constexpr int kPerRow = DV / 4, kStep = kTreeStagers / kPerRow;
+    constexpr int kLoads = Smem::kRows / kStep < 16 ? Smem::kRows / kStep : 16;      // rows of a thread on their way
+    static_assert(Smem::kRows % (kLoads * kStep) == 0, "whole rounds");
     const int mine = tid - kWalkers, sc = mine % kPerRow * 4, sr = mine / kPerRow;
-    const auto stage = [&](int piece) {
+    float4 s[kLoads];
+    const auto ask = [&](int piece, int k0) {
 #pragma unroll
-        for (int k0 = 0; k0 < Smem::kRows; k0 += kLoads * kStep) {
-            float4 s[kLoads];
+        for (int i = 0; i < kLoads; ++i)
+            s[i] = __ldcs(reinterpret_cast<const float4*>(S0 + (piece * Smem::kRows + k0 + sr + i * kStep) * DV + sc));
+    };
+    const auto put = [&](int k0) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                s[i] = __ldcs(reinterpret_cast<const float4*>(S0 + (piece * Smem::kRows + k0 + sr + i * kStep) * DV + sc));
-            if (piece > 0 && k0 == 0) umma::mbar_wait(&sm.done[piece - 1], 0, a.err, kTreeErrBit);
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t lo[NS], hi[NS];
+            split<NS>(s[i].x, s[i].y, lo);
+            split<NS>(s[i].z, s[i].w, hi);
+            const uint32_t to = sc / 64 * (Smem::kRows * 128) + umma::sw128_offset(k0 + sr + i * kStep, sc % 64);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                uint32_t lo[NS], hi[NS];
-                split<NS>(s[i].x, s[i].y, lo);
-                split<NS>(s[i].z, s[i].w, hi);
-                const uint32_t to = sc / 64 * (Smem::kRows * 128) + umma::sw128_offset(k0 + sr + i * kStep, sc % 64);
-#pragma unroll
-                for (int e = 0; e < NS; ++e)
-                    *reinterpret_cast<uint2*>(sm.state + e * Smem::kState + to) = make_uint2(lo[e], hi[e]);
-            }
+            for (int e = 0; e < NS; ++e)
+                *reinterpret_cast<uint2*>(sm.state + e * Smem::kState + to) = make_uint2(lo[e], hi[e]);
         }
     };
     // the products with one piece, by one thread
@@ -203,7 +203,14 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
         umma::commit(&sm.done[piece]);
     };
     if (warp >= kStageWarp) {
-        if (S0) stage(0);
+        if (S0) {
+#pragma unroll 1
+            for (int k0 = 0; k0 < Smem::kRows; k0 += kLoads * kStep) {
+                ask(0, k0);
+                put(k0);
+            }
+            if (Smem::kPieces > 1) ask(1, 0);
+        }
         // what the CTA that follows this one on the SM will read goes into the L2 meanwhile, or memory
         // would idle while this one computes
         const int64_t next = (int64_t)blockIdx.x + a.resident;
@@ -222,22 +229,22 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
         }
         if (tid <= KB) sm.level_end[tid] = 0;
         constexpr int kAhead = 4;                              // quads of alpha and k a thread has on their way
-        for (int e0 = tid; e0 < live * (DK / 4); e0 += kWalkers * kAhead) {
-            float4 g[kAhead], k[kAhead];
+        const int quads = live * (DK / 4);
+        for (int e0 = tid; e0 < quads; e0 += kWalkers * kAhead) {
+            float4 g[kAhead];
+            struct alignas(4 * sizeof(T)) Four { T v[4]; } k[kAhead];
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
-                const int e = e0 + r * kWalkers, i = e / (DK / 4), c = e % (DK / 4) * 4;
-                if (e >= live * (DK / 4)) break;
-                const int64_t at = (tok0 + i * a.H) * DK + c;
+                const int e = min(e0 + r * kWalkers, quads - 1);         // the last one again past the end
+                const int64_t at = (tok0 + e / (DK / 4) * a.H) * DK + e % (DK / 4) * 4;
                 g[r] = __ldcs(reinterpret_cast<const float4*>(a.log_alpha + at));
-                k[r] = load4((const T*)a.k + at);
+                k[r] = *reinterpret_cast<const Four*>((const T*)a.k + at);
             }
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
-                const int e = e0 + r * kWalkers;
-                if (e >= live * (DK / 4)) break;
+                const int e = min(e0 + r * kWalkers, quads - 1);
                 *reinterpret_cast<float4*>(alpha + 4 * e) = make_float4(expf(g[r].x), expf(g[r].y), expf(g[r].z), expf(g[r].w));
-                *reinterpret_cast<float4*>(kf + 4 * e) = k[r];
+                *reinterpret_cast<float4*>(kf + 4 * e) = load4(k[r].v);
             }
         }
         walkers_sync<KB>();
@@ -343,7 +350,11 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
     if (S0) {
         if (tid == 0) multiply(0);
         if (Smem::kPieces > 1 && warp >= kStageWarp) {
-            stage(1);
+            umma::mbar_wait(&sm.done[0], 0, a.err, kTreeErrBit);
+            for (int k0 = 0; k0 < Smem::kRows; k0 += kLoads * kStep) {
+                if (k0 > 0) ask(1, k0);
+                put(k0);
+            }
             umma::fence_smem_to_async();
             stagers_sync();
             if (tid == kWalkers) multiply(1);
