@@ -317,11 +317,11 @@ __global__ void __launch_bounds__(256) glr_setup_kernel(GlrArgs a, ScanWork w, i
     const float* from = bwd ? a.dhT : a.h0;
     float* to = bwd ? a.dh0 : a.hT;
     if ((!a.cu && a.T > 0) || to == nullptr) return;
-    for (int64_t n = me / 32; n < a.N; n += all / 32) {
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {      // a CTA a sequence
         if (a.cu && a.cu[n + 1] > a.cu[n]) continue;
-        const int64_t row = bwd ? n : glr_row(a, n, me % 32 == 0);
+        const int64_t row = bwd ? n : glr_row(a, n, threadIdx.x == 0);
         if (row < 0 || to == from) continue;
-        for (int64_t c = me % 32; c < a.D; c += 32) to[row * a.D + c] = from ? from[row * a.D + c] : 0.f;
+        for (int64_t c = threadIdx.x; c < a.D; c += 256) to[row * a.D + c] = from ? from[row * a.D + c] : 0.f;
     }
 }
 
@@ -752,27 +752,47 @@ glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
     scan_load<T, Aligned, Bwd, NS>(a, w, maps, ring);
 }
 
-template <typename T>
+// One token per sequence: read and written once, V channels a thread (one access each where rows
+// start on 16 bytes: V = 4, or 8 for bf16).
+template <typename T, int V>
 __global__ void __launch_bounds__(128)
 glr_step_kernel(const T* __restrict__ x, const float* __restrict__ log_a, float* __restrict__ state,
                 const int32_t* __restrict__ slots, T* __restrict__ out, int64_t P, int64_t D,
                 int* __restrict__ err)
 {
     const int64_t n = blockIdx.x;
-    const int64_t c = (int64_t)blockIdx.y * 128 + threadIdx.x;
+    const int64_t c = ((int64_t)blockIdx.y * 128 + threadIdx.x) * V;
     if (c >= D) return;
+    struct alignas(V == 1 ? sizeof(T) : V * sizeof(T)) Io { T v[V]; };
+    struct alignas(V == 1 ? 4 : 16) Quad { float v[V == 1 ? 1 : 4]; };
+    constexpr int Q = V == 1 ? 1 : V / 4, W = V == 1 ? 1 : 4;
+    const Io xi = *reinterpret_cast<const Io*>(x + n * D + c);
+    Quad l[Q], s[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) l[q] = *reinterpret_cast<const Quad*>(log_a + n * D + c + W * q);
     int64_t row = n;
+    Io o = {};
     if (slots) {
         row = slots[n];
         if (row >= P && c == 0 && err) atomicOr(err, kErrSeqlens);
         if (row < 0 || row >= P) {
-            IO<T>::store(out, n * D + c, 0.f);
+            *reinterpret_cast<Io*>(out + n * D + c) = o;
             return;
         }
     }
-    const float h = expf(log_a[n * D + c]) * state[row * D + c] + IO<T>::load(x, n * D + c);
-    state[row * D + c] = h;
-    IO<T>::store(out, n * D + c, h);
+    float* at = state + row * D + c;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) s[q] = *reinterpret_cast<const Quad*>(at + W * q);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            s[q].v[e] = expf(l[q].v[e]) * s[q].v[e] + IO<T>::load(xi.v, W * q + e);
+            IO<T>::store(o.v, W * q + e, s[q].v[e]);
+        }
+        *reinterpret_cast<Quad*>(at + W * q) = s[q];
+    }
+    *reinterpret_cast<Io*>(out + n * D + c) = o;
 }
 
 namespace {
@@ -800,7 +820,7 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
         w.tile_ab = w.block_ab + blocks * w.cols * kCh;
         w.range = reinterpret_cast<int2*>(w.tile_ab + w.total * kCh);
         w.zeroed = w.tiles > 1 ? words / 2 : 0;
-        const int64_t work = w.zeroed / 8 + (a.cu ? w.tiles : 0) + (a.cu || a.T == 0 ? a.N * 32 : 0);
+        const int64_t work = w.zeroed / 8 + (a.cu ? w.tiles : 0) + (a.cu || a.T == 0 ? a.N * 256 : 0);
         const int64_t ctas = (work + 255) / 256;
         LaunchScope scope(st, K_GLR_SETUP);
         const cudaError_t s = launch_pdl(glr_setup_kernel, dim3((unsigned)(ctas < 296 ? ctas < 1 ? 1 : ctas : 296)),
@@ -850,18 +870,29 @@ cudaError_t launch_scan_t(const GlrArgs& a, cudaStream_t st)
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st) { return launch_scan_t<false>(a, st); }
 cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st) { return launch_scan_t<true>(a, st); }
 
+namespace {
+
+template <typename T, int V>
+cudaError_t launch_step(const void* x, const float* log_a, float* state, const int32_t* slots, void* out, int64_t N,
+                        int64_t P, int64_t D, int* err, cudaStream_t st)
+{
+    LaunchScope scope(st, K_GLR_STEP);
+    glr_step_kernel<T, V><<<dim3((unsigned)N, (unsigned)((D + 128 * V - 1) / (128 * V))), 128, 0, st>>>(
+        (const T*)x, log_a, state, slots, (T*)out, P, D, err);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_glr_step(const void* x, const float* log_a, float* state, const int32_t* slots,
                             void* out, int64_t N, int64_t P, int64_t D, kda_io_dtype_t io, int* err,
                             cudaStream_t st)
 {
-    LaunchScope scope(st, K_GLR_STEP);
-    const dim3 grid((unsigned)N, (unsigned)((D + 127) / 128));
     if (io == KDA_IO_F32)
-        glr_step_kernel<float><<<grid, 128, 0, st>>>((const float*)x, log_a, state, slots, (float*)out, P, D, err);
-    else
-        glr_step_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>((const __nv_bfloat16*)x, log_a, state, slots,
-                                                            (__nv_bfloat16*)out, P, D, err);
-    return cudaGetLastError();
+        return D % 4 == 0 ? launch_step<float, 4>(x, log_a, state, slots, out, N, P, D, err, st)
+                          : launch_step<float, 1>(x, log_a, state, slots, out, N, P, D, err, st);
+    return D % 8 == 0 ? launch_step<__nv_bfloat16, 8>(x, log_a, state, slots, out, N, P, D, err, st)
+                      : launch_step<__nv_bfloat16, 1>(x, log_a, state, slots, out, N, P, D, err, st);
 }
 
 }  // namespace kda
