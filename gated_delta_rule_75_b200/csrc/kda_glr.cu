@@ -8,7 +8,7 @@
 // warps each do one part of the work for the tiles that pass through a ring of
 // shared-memory stages:
 //   loader       takes tiles and starts their TMA copies, a few tiles ahead;
-//   aggregators  (two groups of kRuns warps, tiles in turn) fold each run of the
+//   aggregators  (groups of kRuns warps, tiles in turn) fold each run of the
 //                tile into (A, B), and the runs into the tile's, and publish that;
 //   carriers     (a warp per stage but one, tiles in turn) put the state that enters the
 //                tile together, from when the tile is taken, of what earlier
@@ -17,7 +17,7 @@
 //                those of the block's earlier tiles, in that order whatever arrives
 //                first; the last tile of a block publishes the block's (A, B), or,
 //                in the last block, the state that enters the next group;
-//   finishers    (two groups of kRuns warps) walk the runs again from their entry
+//   finishers    (groups of kRuns warps) walk the runs again from their entry
 //                states and write the outputs.
 // So loads, arithmetic and the waits of different tiles overlap, a value is the same on
 // every run, and the chain of waits is one hop per group.  CTA c takes tiles c, c + grid, ..
@@ -58,9 +58,13 @@ constexpr int kPolls = 1 << 21;         // about two seconds of polling
 constexpr int kScanBit = 7;             // kErrScanWait
 
 // Warps by role.
-constexpr int kAggWarps = 2 * kRuns, kFinWarps = 2 * kRuns;
+constexpr int kFinGroups = 2, kFinWarps = kFinGroups * kRuns;
+constexpr int agg_groups(bool bwd) { return bwd ? 2 : 3; }
 constexpr int carry_warps(int stages) { return stages - 1; }
-constexpr int scan_threads(int stages) { return 32 * (kAggWarps + kFinWarps + carry_warps(stages) + 1); }
+constexpr int scan_threads(int stages, bool bwd)
+{
+    return 32 * (agg_groups(bwd) * kRuns + kFinWarps + carry_warps(stages) + 1);
+}
 
 // n / d for 0 <= n < 2^31 as (n m) >> s: with 2^k >= d, s = 31 + k and m = ceil(2^s / d), n m / 2^s
 // exceeds n / d by less than n / 2^s 2^-0 <= 2^-k <= 1 / d, which reaches no further integer.
@@ -135,22 +139,33 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
     return d;
 }
 
-// exp of two logarithms of decays: 2^t with t = x / ln 2 rounded, times 1 + r ln 2 for the part r of
-// x / ln 2 that the rounding and the constant dropped, so that large logarithms lose nothing.
-// -200 and below (-inf too) give 0, NaN stays.
+// exp of two logarithms of decays, within a half step and little more.  The hardware's exponential is
+// cheaper, but its errors lean one way and a long memory adds them up (131071 x 1024 fp32: h 5.7e-7 off
+// instead of 1.3e-7).  x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so that r loses nothing),
+// e^r by its Taylor series (r^8 / 8! is below 2^-27), times 2^n.  Below -87.3 (-inf too): 0; NaN stays.
+__device__ __forceinline__ F2 both(float v) { return F2(v, v); }
+__device__ __forceinline__ F2 exp_series(F2 r)
+{
+    F2 p = fma2(r, both(1.f / 5040), both(1.f / 720));
+    p = fma2(p, r, both(1.f / 120));
+    p = fma2(p, r, both(1.f / 24));
+    p = fma2(p, r, both(1.f / 6));
+    p = fma2(p, r, both(0.5f));
+    p = fma2(p, r, both(1.f));
+    return fma2(p, r, both(1.f));
+}
 __device__ __forceinline__ F2 decay2(F2 l)
 {
+    constexpr float log2e = 1.4426950408889634f, ln2_hi = 0.693145751953125f,      // 15 bits: n ln2_hi is exact
+        ln2_lo = (float)(0.69314718055994531 - 0.693145751953125), magic = 12582912.f, least = -87.3f;
     float a, b;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(l.x()), "f"(-200.f));
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(l.y()), "f"(-200.f));
-    constexpr float hi = 1.4426950408889634f, lo = (float)(1.4426950408889634 - (double)hi), ln2 = 0.6931471805599453f;
-    const F2 x(a, b), t = mul2(x, F2(hi, hi));
-    const F2 minus(-t.x(), -t.y());
-    const F2 r = fma2(x, F2(lo, lo), fma2(x, F2(hi, hi), minus));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x()));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y()));
-    const F2 e(a, b);
-    return fma2(mul2(e, F2(ln2, ln2)), r, e);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(l.x()), "f"(least));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(l.y()), "f"(least));
+    const F2 x(a, b), m = fma2(x, both(log2e), both(magic)), n = add2(m, both(-magic));
+    const F2 p = exp_series(fma2(n, both(-ln2_lo), fma2(n, both(-ln2_hi), x)));
+    const F2 q = mul2(p, F2(__int_as_float((__float_as_int(m.x()) << 23) + 0x3f800000),
+                            __int_as_float((__float_as_int(m.y()) << 23) + 0x3f800000)));
+    return F2(l.x() < least ? 0.f : q.x(), l.y() < least ? 0.f : q.y());
 }
 
 // The state behind a run (A, B) entered with h.  A negative A (-0 too): the run holds the
@@ -252,7 +267,8 @@ struct Stage {
     int64_t id;                                                  // tile * cols + column; -1: no more
     int marked;                                                  // whether first / last hold anything
     int plain;                                                   // no marks, all tokens there and in the maps
-    uint64_t taken, full, runs, agg, carried, empty;
+    int folded;                                                  // runs that are there
+    uint64_t taken, full, agg, carried, empty;
     static constexpr uint32_t kCopied = kTile * (La::kPitch + X::kPitch * (Bwd ? 2 : 1));
 
     __device__ __forceinline__ int la_at(int r) const { return Aligned ? r * La::kPitch : off[r] & 0xffff; }
@@ -355,6 +371,7 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
         const bool copies = id >= 0 && w.mapped > 0;
         if (lane == 0) {
             s.id = id;
+            s.folded = 0;
             umma::mbar_arrive(&s.taken);
             if (copies) tma::expect_tx(&s.full, S::kCopied);
             else umma::mbar_arrive(&s.full);
@@ -407,14 +424,14 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
     }
 }
 
-// An aggregator warp: run `run` of every second tile, from tile `group` on.
+// An aggregator warp: run `run` of one tile of agg_groups(Bwd), from tile `group` on.
 template <typename T, bool Aligned, bool Bwd, int NS>
 __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring,
                                                int group, int run)
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
-    for (int64_t q = group;; q += 2) {
+    for (int64_t q = group;; q += agg_groups(Bwd)) {
         S& s = ring[q % NS];
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
@@ -488,9 +505,15 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
         *reinterpret_cast<F2*>(&s.B[run][2 * lane]) = B;
         // the decays written over log_a come before the TMA copy that fills the stage again
         umma::fence_smem_to_async();
-        if (run == 0) {
-            // the tile's other runs are there
-            if (!umma::mbar_wait(&s.runs, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
+        // the last of the tile's runs to be there folds them
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) {
+            __threadfence_block();
+            before = atomicAdd(&s.folded, 1);
+            __threadfence_block();
+        }
+        if (__shfl_sync(0xffffffffu, before, 0) == kRuns - 1) {
             float tA[2] = {1.f, 1.f}, tB[2] = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kRuns; ++k) {
@@ -506,9 +529,9 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
             *reinterpret_cast<float2*>(&s.tB[2 * lane]) = make_float2(tB[0], tB[1]);
             if (at.order + 1 < w.tiles && at.order % kBlock != kBlock - 1)
                 store_words(w.tile_ab + ((int64_t)at.order * w.cols + at.col) * kCh + 2 * lane, tA, tB);
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&s.agg);
         }
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(run == 0 ? &s.agg : &s.runs);
     }
 }
 
@@ -609,14 +632,14 @@ __device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, 
     }
 }
 
-// A finisher warp: run `run` of every second tile, from tile `group` on.
+// A finisher warp: run `run` of one tile of kFinGroups, from tile `group` on.
 template <typename T, bool Aligned, bool Bwd, int NS>
 __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring,
                                             int group, int run)
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
-    for (int64_t q = group;; q += 2) {
+    for (int64_t q = group;; q += kFinGroups) {
         S& s = ring[q % NS];
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
@@ -723,13 +746,13 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 }
 
 template <typename T, bool Aligned, bool Bwd>
-__global__ void __launch_bounds__(scan_threads(ring_stages<T, Aligned, Bwd>()), 1)
+__global__ void __launch_bounds__(scan_threads(ring_stages<T, Aligned, Bwd>(), Bwd), 1)
 glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
 {
     griddep_wait();
     using S = Stage<T, Aligned, Bwd>;
     constexpr int NS = ring_stages<T, Aligned, Bwd>();
-    static_assert(NS >= 3, "the ends take a stage each");
+    static_assert(NS > agg_groups(Bwd) && NS > kFinGroups, "every group meets an end, and ends take a stage each");
     extern __shared__ __align__(128) unsigned char smem[];
     S* ring = reinterpret_cast<S*>(smem);
     int warp = threadIdx.x / 32;
@@ -737,13 +760,13 @@ glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
         S& s = ring[threadIdx.x];
         umma::mbar_init(&s.taken, 1);
         umma::mbar_init(&s.full, 2);             // the copies, and the loader's notes
-        umma::mbar_init(&s.runs, kRuns - 1);
         umma::mbar_init(&s.agg, 1);
         umma::mbar_init(&s.carried, 1);
         umma::mbar_init(&s.empty, kRuns);
         umma::fence_mbar_init();
     }
     __syncthreads();
+    constexpr int kAggWarps = agg_groups(Bwd) * kRuns;
     if (warp < kAggWarps) return scan_aggregate<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
     warp -= kAggWarps;
     if (warp < kFinWarps) return scan_finish<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
@@ -852,7 +875,7 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
     }
     LaunchScope scope(st, Bwd ? K_GLR_BWD : K_GLR_FWD);
     const int64_t sms = device_sm_count();
-    const dim3 grid((unsigned)(w.total < sms ? w.total : sms)), block(scan_threads(ring_stages<T, Aligned, Bwd>()));
+    const dim3 grid((unsigned)(w.total < sms ? w.total : sms)), block(scan_threads(ring_stages<T, Aligned, Bwd>(), Bwd));
     if (w.tiles == 1) return launch_pdl(glr_scan_kernel<T, Aligned, Bwd>, grid, block, smem, st, a, w, maps);
     return launch_coop(kernel, grid, block, smem, st, a, w, maps);
 }
