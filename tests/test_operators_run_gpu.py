@@ -175,3 +175,66 @@ def test_other_stream_and_graphs(cuda_ok):
     r = subprocess.run([sys.executable, "-c", "ROOT = %r\n" % ROOT + CHILD], env=env, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "operators ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+CONCURRENT = r"""
+import sys, torch
+sys.path[:0] = [ROOT, ROOT + "/tests"]
+import gated_delta_rule_75_b200 as kda
+torch.manual_seed(3)
+sets = []
+for D, T in ((256, 20000), (200, 24000), (65, 9000)):
+    x, la = torch.randn(1, T, D, device="cuda"), -torch.rand(1, T, D, device="cuda") * 0.2
+    sets.append((x, la, torch.randn(1, T, D, device="cuda")))
+def one(x, la, dout):
+    h, hT, starts = kda.glr_scan_fwd(x, la, output_starts=True)
+    return h, hT, *kda.glr_scan_bwd(x, la, dout, starts=starts)
+want = [one(*s) for s in sets]
+torch.cuda.synchronize()
+streams = [torch.cuda.Stream() for _ in range(3)]
+for rep in range(4):
+    got = []
+    for k in range(6):
+        with torch.cuda.stream(streams[(k + rep) % 3]):
+            got.append((k % 3, one(*sets[k % 3])))
+    torch.cuda.synchronize()
+    for i, g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i])), (rep, i)
+assert kda.get_error() == 0
+print("streams ok")
+"""
+
+
+def test_scans_on_several_streams_at_once(cuda_ok):
+    """Scans whose tiles wait on one another, each wanting every SM, issued on three streams together:
+    all end, with the results of running them one after another."""
+    from gated_delta_rule_75_b200 import build
+    build.build()
+    env = dict(os.environ)
+    env.pop("KDA_DEBUG", None)
+    r = subprocess.run([sys.executable, "-c", "ROOT = %r\n" % ROOT + CONCURRENT], env=env, capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0 and "streams ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+def test_strong_decays_and_repeated_offsets(cuda_ok, kda):
+    """Decays from none to e^-100 in one tensor, sequences of one token, many empty ones in a row."""
+    lens = [1] * 5 + [0] * 200 + [64, 0, 63, 1, 129] + [0] * 40 + [700]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    g = torch.Generator().manual_seed(17)
+    T, D = cu[-1], 72
+    x = torch.randn((1, T, D), generator=g).cuda()
+    la = (-100 * torch.rand((1, T, D), generator=g) ** 4).cuda()
+    h0 = torch.randn((len(lens), D), generator=g).cuda()
+    dcu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out, hT, starts = kda.glr_scan_fwd(x, la, h0=h0, cu_seqlens=dcu, output_starts=True)
+    H, want, E, eT = R.glr(R.d(x), R.d(la), R.d(h0), cu)
+    R.within(out, H, E, "out")
+    R.within(hT, want, eT, "hT")
+    dx, dla, dh0 = kda.glr_scan_bwd(x, la, x, starts=starts, h0=h0, dhT=h0, cu_seqlens=dcu)
+    want = R.glr_grads(R.d(x), R.d(la), R.d(h0), R.d(x), R.d(h0), cu)
+    R.within(dx, want[0], want[3], "dx")
+    R.within(dla, want[1], want[4], "dlog_a")
+    R.within(dh0, want[2], want[5], "dh0")
