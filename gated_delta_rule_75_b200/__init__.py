@@ -676,7 +676,7 @@ IMAGE_BYTES = 66560   # one (chunk, head) operand image of the tensor-core prefi
 def get_error(device="cuda") -> int:
     """C ABI ``kda_get_error``: takes (reads and clears) the device's error word
     after the work queued on the current stream; bit 0 = malformed cu_seqlens or a
-    slot out of range, bits 1-6 = a bounded device wait gave up."""
+    slot out of range, bits 1-7 = a bounded device wait gave up."""
     dev = torch.device(device)
     word = ctypes.c_int32(0)
     with torch.cuda.device(dev):

@@ -251,6 +251,15 @@ __device__ __forceinline__ F2 load_pair(const float* at, bool on0, bool on1)
     return F2(at && on0 ? at[0] : 0.f, at && on1 ? at[Aligned ? 1 : 32] : 0.f);
 }
 
+// Tokens of a row that are in a sequence: with cu_seqlens (one row) those behind the last sequence
+// are not, and are neither worked on nor written.
+__device__ __forceinline__ int64_t tokens_used(const GlrArgs& a)
+{
+    if (a.cu == nullptr) return a.T;
+    const int64_t n = a.cu[a.N];
+    return n < 0 ? 0 : n < a.T ? n : a.T;
+}
+
 // One stage of the ring.
 template <typename T, bool Aligned, bool Bwd>
 struct Stage {
@@ -354,6 +363,7 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32;
     const int R = Aligned ? 1 : 1 << w.log_r;
+    const int64_t used = tokens_used(a);
     int64_t next = blockIdx.x;
     int ends = 0;
     for (int64_t q = 0; ends < carry_warps(NS); ++q, next += gridDim.x) {
@@ -404,7 +414,7 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
             const bool marked = a.cu ? range.y > range.x : begins || ends_here;
             if (lane == 0) {
                 s.marked = marked;
-                s.plain = !marked && at.t0 + kTile <= a.T && at.row0 + kTile <= w.mapped;
+                s.plain = !marked && at.t0 + kTile <= used && at.row0 + kTile <= w.mapped;
             }
             if (marked) {
                 for (int t = lane; t < kTile; t += 32) {
@@ -431,6 +441,7 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
+    const int64_t used = tokens_used(a);
     for (int64_t q = group;; q += agg_groups(Bwd)) {
         S& s = ring[q % NS];
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
@@ -455,7 +466,7 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
                     B = mul2(S::La::get(s.la, s.la_at(r0 + k), lane), add2(B, S::X::get(s.y, s.x_at(r0 + k), lane)));
             }
         } else {
-            const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile);   // tokens that exist
+            const int live = (int)(used - at.t0 < kTile ? used - at.t0 : kTile);   // tokens that exist (or less than none)
             const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
             const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
             for (int r = r0; r < r0 + kSteps && r < live; ++r) {
@@ -639,11 +650,12 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 {
     using S = Stage<T, Aligned, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
+    const int64_t used = tokens_used(a);
     for (int64_t q = group;; q += kFinGroups) {
         S& s = ring[q % NS];
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
-        const int live = (int)(a.T - at.t0 < kTile ? a.T - at.t0 : kTile);       // tokens that exist
+        const int live = (int)(used - at.t0 < kTile ? used - at.t0 : kTile);     // tokens that exist (or less than none)
         const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
         const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
         F2 enter(0.f, 0.f);                      // backward: the kept entry state, asked for before the wait

@@ -417,14 +417,15 @@ KDA_API kda_status_t kda_affine_prefix(const float* maps, const float* offs, con
  *  starts      [B, ceil(T / KDA_GLR_TILE), D] fp32 or NULL: written with the state
  *              before tokens 0, KDA_GLR_TILE, 2 KDA_GLR_TILE, .. of every row (h0 of its
  *              sequence where that token begins one), which the backward takes.
- *              (A row of starts holds arbitrary values where malformed cu_seqlens leave
- *              the token in no sequence.)
  *  cu_seqlens  as for kda_chunk_fwd (x, log_a, out and starts then have a leading axis
- *              of 1, B is the number of sequences, N = B)
+ *              of 1, B is the number of sequences, N = B).  Of malformed offsets, one
+ *              kind has a defined result beside bit 0 of the error word: with
+ *              cu_seqlens[B] < T the tokens behind the last sequence are not read and
+ *              their rows of out (dx, dlog_a in the backward) left as they were.
  * Any D >= 1 up to 2^20, fewer than 2^31 - 128 tokens in all; D, B or T of 0 is a no-op
  * apart from hT = h0.  The state is fp32 throughout; out is
  * rounded once.  A call over more than one tile of the token axis uses a workspace of
- * about 9 bytes per tile and channel from the library's pool.  The result is the same
+ * about 10 bytes per tile and channel from the library's pool.  The result is the same
  * on every run.
  *
  * kda_glr_scan_fwd_slots -- h0 = hT = state_pool[slots[n]] ([P, D] fp32), with the
@@ -439,7 +440,8 @@ KDA_API kda_status_t kda_affine_prefix(const float* maps, const float* offs, con
  *   NULL if not wanted.
  * kda_glr_step -- one token per sequence: x, log_a, out [N, D], state [N, D] in place.
  *   kda_glr_step_slots: state_pool [P, D]; a negative slot gives a zero output row.
- * Outputs must not overlap inputs or one another except as stated.
+ * Outputs must not overlap inputs or one another except as stated.  A scan of more than
+ * one tile is a cooperative launch: it starts once all its blocks fit on the GPU at once.
  */
 #define KDA_GLR_TILE 64
 KDA_API kda_status_t kda_glr_scan_fwd(const void* x, const float* log_a, const float* h0, void* out,
@@ -526,8 +528,8 @@ KDA_API kda_status_t kda_tree_commit(const void* k, const void* v, const float* 
  * kda_group_norm_bwd -- gradients for dout [M, G, d]: dx and dgate (required exactly
  *   when gate is given) in io_dtype; dweight, dbias fp32 in the layout of weight and
  *   bias, or NULL if not wanted (dweight is also defined for weight NULL).  The sums over tokens
- *   are fp32, in a fixed order (the same result on every run), through a workspace of at
- *   most 16 MB.  M = 0 sets dweight and dbias to zero.
+ *   are fp32, in a fixed order (the same result on every run), through a workspace
+ *   of at most 16 MB, or twice the size of weight and bias gradients where that is more.  M = 0 sets dweight and dbias to zero.
  */
 typedef enum {
     KDA_ACT_NONE = 0,

@@ -211,3 +211,24 @@ def test_not_a_number_stays_in_its_sequence_and_channel(kda):
     want[150:300, 3] = True
     want[20:100, 1] = True
     assert torch.equal(bad, want) and int((~torch.isfinite(hT)).sum()) == 2
+
+
+@pytest.mark.parametrize("io,D", [("f32", 40), ("bf16", 7)])
+@pytest.mark.parametrize("end", [0, 1, 64, 90, 150])
+def test_rows_behind_the_last_sequence_stay(kda, io, D, end):
+    """Offsets that end before the tokens do (padding behind the last sequence) are reported; what lies in
+    a sequence is computed, what lies behind is not written."""
+    T = 200
+    lens = [end - end // 3, 0, end // 3]
+    cu, dcu = offsets(lens)
+    x, la, h0 = inputs(1, T, D, io, 31 + end, N=3)
+    x[:, end:] = float("nan")
+    out = torch.full_like(x, 5.0)
+    hT = torch.empty_like(h0)
+    with pytest.raises(kda.KDAError) as e:
+        kda.glr_scan_fwd(x, la, h0=h0, cu_seqlens=dcu, out=out, hT=hT)
+    assert e.value.status == kda.KDA_ERR_INVALID_ARG
+    H, want, E, eT = R.glr(R.d(x), R.d(la), R.d(h0), cu)
+    R.within(out[:, :end], H[:, :end], E[:, :end], "out")
+    R.within(hT, want, eT, "hT")
+    assert bool((out[:, end:] == 5).all())
