@@ -141,31 +141,30 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
 
 // exp of two logarithms of decays, within a half step and little more.  The hardware's exponential is
 // cheaper, but its errors lean one way and a long memory adds them up (131071 x 1024 fp32: h 5.7e-7 off
-// instead of 1.3e-7).  x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so that r loses nothing),
-// e^r by its Taylor series (r^8 / 8! is below 2^-27), times 2^n.  Below -87.3 (-inf too): 0; NaN stays.
+// instead of 1.3e-7).  x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so that r loses nothing);
+// e^r = 1 + r + r^2 g(r), g by interpolation of degree 4 at the Chebyshev points of that interval (0.2
+// half steps off); times 2^n.  n = -127, where x is cut off (-inf too), makes the scale and the decay 0;
+// NaN stays.
 __device__ __forceinline__ F2 both(float v) { return F2(v, v); }
-__device__ __forceinline__ F2 exp_series(F2 r)
-{
-    F2 p = fma2(r, both(1.f / 5040), both(1.f / 720));
-    p = fma2(p, r, both(1.f / 120));
-    p = fma2(p, r, both(1.f / 24));
-    p = fma2(p, r, both(1.f / 6));
-    p = fma2(p, r, both(0.5f));
-    p = fma2(p, r, both(1.f));
-    return fma2(p, r, both(1.f));
-}
 __device__ __forceinline__ F2 decay2(F2 l)
 {
     constexpr float log2e = 1.4426950408889634f, ln2_hi = 0.693145751953125f,      // 15 bits: n ln2_hi is exact
-        ln2_lo = (float)(0.69314718055994531 - 0.693145751953125), magic = 12582912.f, least = -87.3f;
+        ln2_lo = (float)(0.69314718055994531 - 0.693145751953125), magic = 12582912.f,     // 1.5 * 2^23: rounds
+        least = (float)(-127 * 0.69314718055994531);
     float a, b;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(l.x()), "f"(least));
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(l.y()), "f"(least));
     const F2 x(a, b), m = fma2(x, both(log2e), both(magic)), n = add2(m, both(-magic));
-    const F2 p = exp_series(fma2(n, both(-ln2_lo), fma2(n, both(-ln2_hi), x)));
-    const F2 q = mul2(p, F2(__int_as_float((__float_as_int(m.x()) << 23) + 0x3f800000),
-                            __int_as_float((__float_as_int(m.y()) << 23) + 0x3f800000)));
-    return F2(l.x() < least ? 0.f : q.x(), l.y() < least ? 0.f : q.y());
+    const F2 r = fma2(n, both(-ln2_lo), fma2(n, both(-ln2_hi), x));
+    F2 p = fma2(r, both(0.0013926198f), both(0.00836319f));
+    p = fma2(p, r, both(0.041666556f));
+    p = fma2(p, r, both(0.16666576f));
+    p = fma2(p, r, both(0.5f));
+    p = fma2(p, r, both(1.f));
+    p = fma2(p, r, both(1.f));
+    // the low bits of m are n; n + 127 is the scale's exponent
+    return mul2(p, F2(__int_as_float((__float_as_int(m.x()) << 23) + 0x3f800000),
+                      __int_as_float((__float_as_int(m.y()) << 23) + 0x3f800000)));
 }
 
 // The state behind a run (A, B) entered with h.  A negative A (-0 too): the run holds the
