@@ -153,8 +153,8 @@ def _ptr(t):
 
 
 def _check(t, name, dtype, shape, device):
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
+        return                    # the usual case at a fifth of a microsecond
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -432,14 +432,17 @@ def gdn_chunk_bwd(q, k, v, log_a, beta, scale, dout, h0=None, dhT=None, cu_seqle
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's address, by device index
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _call(name, dev, *args):
-    """Calls a C entry point on ``dev``'s current stream, with ``dev`` current; tensors in
-    ``args`` become their device addresses.  Raises KDAError on a failed status."""
-    if dev.type != "cuda":
+    """Calls a C entry point on ``dev``'s current stream, with ``dev`` current.  Raises
+    KDAError on a failed status."""
+    index = dev.index
+    if index is None or dev.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a CUDA device, not {dev}")
     fn = getattr(_lib or _load(), name)
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-    index = dev.index
     if torch.cuda.current_device() == index:
         st = fn(*args, _raw_stream(index))
     else:
@@ -495,8 +498,8 @@ def glr_scan_fwd(x, log_a, h0=None, cu_seqlens=None, out=None, hT=None, output_f
         _check(slots, "slots", torch.int32, (N,), dev)
         P = state_pool.shape[0]
         _check(state_pool, "state_pool", torch.float32, (P, D), dev)
-        _call("kda_glr_scan_fwd_slots", dev, x, log_a, state_pool, slots, out, starts, cu_seqlens,
-              N, T, P, D, io)
+        _call("kda_glr_scan_fwd_slots", dev, x.data_ptr(), log_a.data_ptr(), state_pool.data_ptr(),
+              slots.data_ptr(), out.data_ptr(), _addr(starts), _addr(cu_seqlens), N, T, P, D, io)
         hT = state_pool
     else:
         if state_pool is not None:
@@ -507,7 +510,8 @@ def glr_scan_fwd(x, log_a, h0=None, cu_seqlens=None, out=None, hT=None, output_f
             _check(hT, "hT", torch.float32, (N, D), dev)
         elif output_final_state:
             hT = torch.empty((N, D), dtype=torch.float32, device=dev)
-        _call("kda_glr_scan_fwd", dev, x, log_a, h0, out, hT, starts, cu_seqlens, N, T, D, io)
+        _call("kda_glr_scan_fwd", dev, x.data_ptr(), log_a.data_ptr(), _addr(h0), out.data_ptr(),
+              _addr(hT), _addr(starts), _addr(cu_seqlens), N, T, D, io)
     return (out, hT, starts) if output_starts else (out, hT)
 
 
@@ -531,8 +535,9 @@ def glr_scan_bwd(x, log_a, dout, starts=None, h0=None, dhT=None, cu_seqlens=None
             _check(t, name, torch.float32, (N, D), dev)
     dx, dlog_a = torch.empty_like(x), torch.empty_like(log_a)
     dh0 = torch.empty((N, D), dtype=torch.float32, device=dev) if need_dh0 else None
-    _call("kda_glr_scan_bwd", dev, x, log_a, h0, starts, dout, dhT, dx, dlog_a, dh0, cu_seqlens,
-          N, T, D, io)
+    _call("kda_glr_scan_bwd", dev, x.data_ptr(), log_a.data_ptr(), _addr(h0), _addr(starts),
+          dout.data_ptr(), _addr(dhT), dx.data_ptr(), dlog_a.data_ptr(), _addr(dh0),
+          _addr(cu_seqlens), N, T, D, io)
     return dx, dlog_a, dh0
 
 
@@ -554,10 +559,12 @@ def glr_step(x, log_a, state, out=None, slots=None):
         _check(slots, "slots", torch.int32, (N,), dev)
         P = state.shape[0]
         _check(state, "state", torch.float32, (P, D), dev)
-        _call("kda_glr_step_slots", dev, x, log_a, state, slots, out, N, P, D, io)
+        _call("kda_glr_step_slots", dev, x.data_ptr(), log_a.data_ptr(), state.data_ptr(),
+              slots.data_ptr(), out.data_ptr(), N, P, D, io)
     else:
         _check(state, "state", torch.float32, (N, D), dev)
-        _call("kda_glr_step", dev, x, log_a, state, out, N, D, io)
+        _call("kda_glr_step", dev, x.data_ptr(), log_a.data_ptr(), state.data_ptr(), out.data_ptr(),
+              N, D, io)
     return out
 
 
@@ -599,8 +606,9 @@ def tree_fwd(q, k, v, log_alpha, beta, state, parents, scale, num_nodes=None, sl
         out = (torch.empty if num_nodes is None else torch.zeros)((N, K, H, dv), dtype=k.dtype, device=dev)
     else:
         _check(out, "out", k.dtype, (N, K, H, dv), dev)
-    _call("kda_tree_fwd", dev, q, k, v, log_alpha, beta, state, slots, parents, num_nodes, out,
-          N, P, K, H, dk, dv, float(scale), io)
+    _call("kda_tree_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
+          beta.data_ptr(), state.data_ptr(), _addr(slots), parents.data_ptr(), _addr(num_nodes),
+          out.data_ptr(), N, P, K, H, dk, dv, float(scale), io)
     return out
 
 
@@ -610,7 +618,8 @@ def tree_commit(k, v, log_alpha, beta, state, parents, accepted, slots=None):
     for :func:`tree_fwd`.  Returns ``state``."""
     N, P, K, H, dk, dv, dev, io = _tree_args(k, v, log_alpha, beta, state, parents, slots)
     _check(accepted, "accepted", torch.int32, (N,), dev)
-    _call("kda_tree_commit", dev, k, v, log_alpha, beta, state, slots, parents, accepted,
+    _call("kda_tree_commit", dev, k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(),
+          state.data_ptr(), _addr(slots), parents.data_ptr(), accepted.data_ptr(),
           N, P, K, H, dk, dv, io)
     return state
 
@@ -649,8 +658,8 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="s
         out = torch.empty_like(x)
     else:
         _check(out, "out", x.dtype, x.shape, x.device)
-    _call("kda_group_norm_fwd", x.device, x, gate, weight, bias, out, M, G, d, per_group,
-          1 if center else 0, float(eps), _ACT[activation], io)
+    _call("kda_group_norm_fwd", x.device, x.data_ptr(), _addr(gate), _addr(weight), _addr(bias),
+          out.data_ptr(), M, G, d, per_group, 1 if center else 0, float(eps), _ACT[activation], io)
     return out
 
 
@@ -665,8 +674,9 @@ def group_norm_bwd(x, weight, dout, bias=None, gate=None, eps=1e-5, activation="
     dgate = torch.empty_like(x) if gate is not None else None
     dweight = torch.empty_like(weight) if weight is not None else None
     dbias = torch.empty_like(bias) if bias is not None else None
-    _call("kda_group_norm_bwd", x.device, x, gate, weight, bias, dout, dx, dgate, dweight, dbias,
-          M, G, d, per_group, 1 if center else 0, float(eps), _ACT[activation], io)
+    _call("kda_group_norm_bwd", x.device, x.data_ptr(), _addr(gate), _addr(weight), _addr(bias),
+          dout.data_ptr(), dx.data_ptr(), _addr(dgate), _addr(dweight), _addr(dbias), M, G, d,
+          per_group, 1 if center else 0, float(eps), _ACT[activation], io)
     return dx, dgate, dweight, dbias
 
 
