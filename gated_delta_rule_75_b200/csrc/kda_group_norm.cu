@@ -93,17 +93,23 @@ __device__ __forceinline__ float slot_sum(float v)
     return v;
 }
 
-// fp32 I/O: within 3 half steps.  bf16 I/O: the exponential's argument is rounded once more and the
-// reciprocal is the hardware's, |z| + 4 half steps of 2^-24 together, far below the output's own 2^-8; it
-// takes 4 instructions for about 20, which is what bounded the kernel (65536 x 32 x 128: 411 -> 2xx us).
+// The reciprocal is the hardware's (2 half steps of 2^-24) in place of a division of ten instructions.
+// fp32 I/O: with expf, within 6 half steps.  bf16 I/O: the exponential's argument is rounded once more,
+// |z| + 4 half steps, far below the output's own 2^-8; 4 instructions for about 20, which is what bounded
+// the forward (65536 x 32 x 128: 411 -> 267 us).
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 template <typename T> __device__ __forceinline__ float sigmoid(float z);
-template <> __device__ __forceinline__ float sigmoid<float>(float z) { return 1.f / (1.f + expf(-z)); }
+template <> __device__ __forceinline__ float sigmoid<float>(float z) { return reciprocal(1.f + expf(-z)); }
 template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float z)
 {
-    float e, r;
+    float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+    return reciprocal(1.f + e);
 }
 
 // Which rows a slot takes.
@@ -325,12 +331,12 @@ group_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ gate,
     }
 }
 
-// dst[c] = sum over rows r of part[r][c]: 32 columns a CTA, 8 row groups, added in a fixed order.
-__global__ void __launch_bounds__(256)
+// dst[c] = sum over rows r of part[r][c]: 32 columns a CTA, 32 row groups, added in a fixed order.
+__global__ void __launch_bounds__(1024)
 group_norm_wgrad_kernel(const float* __restrict__ wpart, const float* __restrict__ bpart,
                         float* __restrict__ dweight, float* __restrict__ dbias, int64_t rows, int64_t cols)
 {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const float* part = blockIdx.y == 0 ? wpart : bpart;
     float* dst = blockIdx.y == 0 ? dweight : dbias;
     if (dst == nullptr) return;
@@ -338,14 +344,15 @@ group_norm_wgrad_kernel(const float* __restrict__ wpart, const float* __restrict
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < cols)
-        for (int64_t r = ty; r < rows; r += 8) s += part[r * cols + c];
+#pragma unroll 8
+        for (int64_t r = ty; r < rows; r += 32) s += part[r * cols + c];
     red[ty][tx] = s;
     __syncthreads();
-    if (ty == 0 && c < cols) {
+    // warp ty adds up column ty
+    s = red[tx][ty];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) s += red[k][tx];
-        dst[c] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (tx == 0 && (int64_t)blockIdx.x * 32 + ty < cols) dst[(int64_t)blockIdx.x * 32 + ty] = s;
 }
 
 namespace {
@@ -414,7 +421,7 @@ cudaError_t norm_bwd(const GroupNormArgs& a, cudaStream_t st)
     }
     if (one == 0) return cudaSuccess;
     LaunchScope scope(st, K_GNORM_WGRAD);
-    group_norm_wgrad_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(wpart, bpart, a.dweight, a.dbias,
+    group_norm_wgrad_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, st>>>(wpart, bpart, a.dweight, a.dbias,
                                                                                   rows, cols);
     return cudaGetLastError();
 }
