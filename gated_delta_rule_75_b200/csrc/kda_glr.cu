@@ -41,6 +41,11 @@
 // dlog_a_t = c_t h_{t-1} needs the forward states too; they are walked again inside
 // the tile from its kept entry state (starts), so the pass reads x, log_a, dout and
 // writes dx, dlog_a once.
+//
+// Measured (copies run at 6.46 TB/s): 8 x 8192 x 4096 bf16, 2.15 GB, 400 us when the SM clock is at
+// its top and 440 under the power cap (1660 MHz); 131071 x 1024 fp32, 1.61 GB, 293 us; 8 x 8192 x
+// 4096 in registers, a CTA a tile, 644.  Tiles of 64 x 64: their ring (8 stages of 28 KiB for bf16)
+// keeps about 190 KiB of an SM on its way or in work for the 5 us from a tile's copy to its last store.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_tma.cuh"

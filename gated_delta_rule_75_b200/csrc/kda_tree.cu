@@ -11,15 +11,19 @@
 // decays come from walking up the path one factor at a time: every factor is at most 1, so any
 // decay rate is safe, and the last one is the row that multiplies S0.
 //
-// Bound by memory: a head's state is 64 KiB at d = 128, its 16 drafted tokens 24 KiB; next to
-// that 1 MFLOP of products with S0 (4 for 64 nodes), which mma.sync took 1.6 (6.5) us of an SM for,
-// so they are on tcgen05: 0.3 (0.8) us.  One CTA of 384 threads for one (sequence, head), two of
-// them on an SM up to 32 nodes so that one's loads cover another's arithmetic.  Warps 0 - 7:
-//   1. alpha, k into shared memory (q, v on their way into the L2); depths, order by depth;
-//   2. eight lanes a node walk up its path, every lane 16 (8) channels: the dots with every
-//      ancestor (three shuffles each), then the node's two rows, kept in registers;
+// A head's state is 64 KiB at d = 128, its 16 drafted tokens 24 KiB: 2 us of an SM's share of the
+// memory, next to 1 MFLOP of products with S0 (4 for 64 nodes), which mma.sync took 1.6 (6.5) us of
+// an SM for, so they are on tcgen05: 0.3 (0.8) us.  What bounds the kernel is the latency of its
+// steps: 18,700 (24,500) cycles, of which 4,700 are loads, 4,500 (3,900) the products and 3,100
+// (6,300) the levels; three CTAs of an SM cover one another up to 16 nodes, two up to 32, and the
+// state of the CTA that follows is brought into the L2 meanwhile.  64 x 16 nodes, 32 heads: 58 us, 3.2 TB/s
+// (two CTAs, all of S0 at once: 72); 40 x 61 nodes: 126 us.
+// One CTA for one (sequence, head).  The walking warps, eight lanes a node:
+//   1. alpha, k into shared memory; depths, order by depth;
+//   2. walk up the node's path, every lane 16 (8) channels: the dots with every ancestor (three
+//      shuffles each), then the node's two rows, kept in registers;
 //   3. the rows (keys, then queries) as bf16 summands in shared memory.
-// Meanwhile warps 8 - 11 bring S0 there, as bf16 summands too.  Then one thread issues the
+// Meanwhile four more warps bring S0 there, as bf16 summands too.  Then one thread issues the
 // product, transposed, D^T = S0^T rows^T: M = dv, N = rows, so that N and the tensor memory follow
 // the number of nodes.  Rows and S0 are split into two bf16 summands each (three for fp32 I/O) and
 // the products down to 2^-17 (2^-25) of the whole are summed in fp32.  Then, all warps:
