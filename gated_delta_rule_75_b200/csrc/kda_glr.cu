@@ -59,6 +59,7 @@ constexpr int kRuns = 4;                // runs of a tile, one a warp
 constexpr int kSteps = kTile / kRuns;   // tokens of a run
 constexpr int kBlock = 8;               // tiles of a block
 constexpr int kBlocks = 8;              // blocks of a group
+static_assert(kBlocks <= kBlock, "words of a group and of a block are held in the same registers");
 constexpr int kPolls = 1 << 21;         // about two seconds of polling
 constexpr int kScanBit = 7;             // kErrScanWait
 
@@ -71,8 +72,8 @@ constexpr int scan_threads(int stages, bool bwd)
     return 32 * (agg_groups(bwd) * kRuns + kFinWarps + carry_warps(stages) + 1);
 }
 
-// n / d for 0 <= n < 2^31 as (n m) >> s: with 2^k >= d, s = 31 + k and m = ceil(2^s / d), n m / 2^s
-// exceeds n / d by less than n / 2^s 2^-0 <= 2^-k <= 1 / d, which reaches no further integer.
+// n / d for 0 <= n < 2^31 as (n m) >> s: with 2^k >= d, s = 31 + k and m = ceil(2^s / d), n m / 2^s is n / d
+// and less than n / 2^s < 2^-k <= 1 / d more, which reaches no further integer.
 struct Divide {
     uint32_t m, s;
     Divide() = default;
@@ -86,18 +87,18 @@ struct Divide {
     __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> s); }
 };
 
-// Workspace: the groups' entry states and the blocks' and tiles' (A, B), all zeroed by the setup
-// kernel; with cu_seqlens each tile's range of offsets.  A column is one block of kCh
+// Workspace: for every group its entry state and the (A, B) of its blocks but the last, which the next
+// group's entry state holds, side by side so that one wait asks for them together; the tiles' (A, B). All
+// zeroed by the setup kernel; with cu_seqlens each tile's range of offsets.  A column is one block of kCh
 // channels of one row of the token axis; tiles, blocks and groups are numbered in the order of
 // the scan (from the end in the backward).
 struct ScanWork {
-    unsigned long long* entry;     // [groups][cols][kCh]: words (1, state)
-    unsigned long long* block_ab;  // [blocks][cols][kCh]: words (A, B)
+    unsigned long long* groups;    // [groups][kBlocks][cols][kCh]: words (1, entry state), then (A, B) of blocks
     unsigned long long* tile_ab;   // [tiles][cols][kCh]: words (A, B)
     int2* range;                   // [tiles]: offsets cu[x .. y - 1] lie in [first token, first + kTile]
     int64_t cols, tiles, total;    // total = tiles * cols
     Divide by_cols, by_blocks;     // by cols, and by the columns of one row
-    int64_t zeroed;                // 16-byte words from entry on
+    int64_t zeroed;                // 16-byte words from groups on
     uint32_t blocks;               // columns of one row
     int log_r;                     // R = 1 << log_r rows of the tensor are one row of the tensor maps
     int64_t mapped;                // tokens (over all rows) that the tensor maps cover
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(256) glr_setup_kernel(GlrArgs a, ScanWork w, i
     griddep_wait();
     griddep_launch_dependents();
     const int64_t me = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
-    for (int64_t k = me; k < w.zeroed; k += all) reinterpret_cast<uint4*>(w.entry)[k] = make_uint4(0, 0, 0, 0);
+    for (int64_t k = me; k < w.zeroed; k += all) reinterpret_cast<uint4*>(w.groups)[k] = make_uint4(0, 0, 0, 0);
     if (a.cu) {
         // few offsets are searched in shared memory: one trip to memory, not one per step
         constexpr int kHeld = 4096;
@@ -611,35 +612,36 @@ __device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, 
         const float2 tA = *reinterpret_cast<const float2*>(&s.tA[2 * lane]);
         const float2 tB = *reinterpret_cast<const float2*>(&s.tB[2 * lane]);
         const float A[2] = {tA.x, tA.y}, B[2] = {tB.x, tB.y};
+        unsigned long long* group = w.groups + g * kBlocks * pitch + lane2;
         if (more && last && blocks < kBlocks - 1) {
             const float bA[2] = {chain(rA[0], A[0]), chain(rA[1], A[1])};
             const float bB[2] = {leave(A[0], B[0], rB[0]), leave(A[1], B[1], rB[1])};
-            store_words(w.block_ab + block * pitch + lane2, bA, bB);
+            store_words(group + (blocks + 1) * pitch, bA, bB);
         }
-        // the group's entry state, its earlier blocks, then the run
-        float carry[2] = {0.f, 0.f}, pA[2] = {1.f, 1.f}, pB[2] = {0.f, 0.f};
-        if (blocks > 0) {
-            await_words(w.block_ab + (block - blocks) * pitch + lane2, pitch, blocks, v0, v1, a.err);
+        // the group's entry state (the first group has none), its earlier blocks, then the run
+        const int none = g == 0 ? 1 : 0, count = blocks + 1 - none;
+        float carry[2] = {0.f, 0.f};
+        if (count > 0) {
+            await_words(group + none * pitch, pitch, count, v0, v1, a.err);
+            float pA[2] = {1.f, 1.f}, pB[2] = {0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < kBlocks - 1; ++k)
-                if (k < blocks) append(pA, pB, v0[k], v1[k]);
-        }
+            for (int k = 0; k < kBlocks; ++k)
+                if (k < count && k + none > 0) append(pA, pB, v0[k], v1[k]);
+            if (none == 0) {
+                carry[0] = __uint_as_float((unsigned)(v0[0] >> 32));
+                carry[1] = __uint_as_float((unsigned)(v1[0] >> 32));
+            }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            rB[e] = leave(rA[e], rB[e], pB[e]);
-            rA[e] = chain(pA[e], rA[e]);
-        }
-        if (g > 0) {
-            unsigned long long e0[1], e1[1];
-            await_words(w.entry + g * pitch + lane2, pitch, 1, e0, e1, a.err);
-            carry[0] = __uint_as_float((unsigned)(e0[0] >> 32));
-            carry[1] = __uint_as_float((unsigned)(e1[0] >> 32));
+            for (int e = 0; e < 2; ++e) {
+                rB[e] = leave(rA[e], rB[e], pB[e]);
+                rA[e] = chain(pA[e], rA[e]);
+            }
         }
         carry[0] = leave(rA[0], rB[0], carry[0]);
         carry[1] = leave(rA[1], rB[1], carry[1]);
         if (more && last && blocks == kBlocks - 1) {
             const float one[2] = {1.f, 1.f}, out[2] = {leave(A[0], B[0], carry[0]), leave(A[1], B[1], carry[1])};
-            store_words(w.entry + (g + 1) * pitch + lane2, one, out);
+            store_words(group + kBlocks * pitch, one, out);
         }
         *reinterpret_cast<float2*>(&s.carry[2 * lane]) = make_float2(carry[0], carry[1]);
         __syncwarp();
@@ -851,12 +853,11 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
     // tokens want looking at
     if (w.tiles > 1 || a.cu || a.T == 0) {
         const int64_t blocks = (w.tiles + kBlock - 1) / kBlock, groups = (blocks + kBlocks - 1) / kBlocks;
-        const int64_t words = ((groups + blocks) * w.cols + w.total) * kCh, ranges = (w.tiles + 1) / 2 * 2;
+        const int64_t words = (groups * kBlocks * w.cols + w.total) * kCh, ranges = (w.tiles + 1) / 2 * 2;
         const cudaError_t e = buf.alloc((size_t)((words + ranges) * 8), st);
         if (e != cudaSuccess) return e;
-        w.entry = static_cast<unsigned long long*>(buf.ptr);
-        w.block_ab = w.entry + groups * w.cols * kCh;
-        w.tile_ab = w.block_ab + blocks * w.cols * kCh;
+        w.groups = static_cast<unsigned long long*>(buf.ptr);
+        w.tile_ab = w.groups + groups * kBlocks * w.cols * kCh;
         w.range = reinterpret_cast<int2*>(w.tile_ab + w.total * kCh);
         w.zeroed = w.tiles > 1 ? words / 2 : 0;
         const int64_t work = w.zeroed / 8 + (a.cu ? w.tiles : 0) + (a.cu || a.T == 0 ? a.N * 256 : 0);
