@@ -47,6 +47,7 @@
 // 4096 in registers, a CTA a tile, 644.  Tiles of 64 x 64: their ring (8 stages of 28 KiB for bf16)
 // keeps about 190 KiB of an SM on its way or in work for the 5 us from a tile's copy to its last store.
 #include "kda_common.cuh"
+#include "kda_f32x2.cuh"
 #include "kda_internal.h"
 #include "kda_tma.cuh"
 #include "kda_umma.cuh"
@@ -118,40 +119,12 @@ __device__ __forceinline__ void store_words(unsigned long long* p, const float (
     asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(a), "l"(b) : "memory");
 }
 
-// Two channels at once: a register pair, and one instruction for both.
-struct F2 {
-    unsigned long long v;
-    __device__ __forceinline__ F2() {}
-    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ float x() const { return __uint_as_float((unsigned)v); }
-    __device__ __forceinline__ float y() const { return __uint_as_float((unsigned)(v >> 32)); }
-};
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return d;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-
 // exp of two logarithms of decays, within a half step and little more.  The hardware's exponential is
 // cheaper, but its errors lean one way and a long memory adds them up (131071 x 1024 fp32: h 5.7e-7 off
 // instead of 1.3e-7).  x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so that r loses nothing);
 // e^r = 1 + r + r^2 g(r), g by interpolation of degree 4 at the Chebyshev points of that interval (0.2
 // half steps off); times 2^n.  n = -127, where x is cut off (-inf too), makes the scale and the decay 0;
 // NaN stays.
-__device__ __forceinline__ F2 both(float v) { return F2(v, v); }
 __device__ __forceinline__ F2 decay2(F2 l)
 {
     constexpr float log2e = 1.4426950408889634f, ln2_hi = 0.693145751953125f,      // 15 bits: n ln2_hi is exact

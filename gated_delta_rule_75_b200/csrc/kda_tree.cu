@@ -29,6 +29,7 @@
 // the products down to 2^-17 (2^-25) of the whole are summed in fp32.  Then, all warps:
 //   4. D^T to shared memory; level by level, a warp a node: u_i and o_i.
 #include "kda_common.cuh"
+#include "kda_f32x2.cuh"
 #include "kda_internal.h"
 #include "kda_umma.cuh"
 
@@ -55,6 +56,17 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
                        __uint_as_float(u.y & 0xffff0000u));
 }
 using umma::pack_bf16;
+
+// Four channels in shared memory, as pairs.
+struct Four { F2 a, b; };
+__device__ __forceinline__ Four four(const float* p)
+{
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+    Four f;
+    f.a.v = u.x;
+    f.b.v = u.y;
+    return f;
+}
 
 // (x, y) as NS bf16 pairs whose sum is within 2^-(8 NS + 1) of each: s[0] the largest.
 template <int NS>
@@ -236,13 +248,13 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
         const int quads = live * (DK / 4);
         for (int e0 = tid; e0 < quads; e0 += kWalkers * kAhead) {
             float4 g[kAhead];
-            struct alignas(4 * sizeof(T)) Four { T v[4]; } k[kAhead];
+            struct alignas(4 * sizeof(T)) Raw { T v[4]; } k[kAhead];
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
                 const int e = min(e0 + r * kWalkers, quads - 1);         // the last one again past the end
                 const int64_t at = (tok0 + e / (DK / 4) * a.H) * DK + e % (DK / 4) * 4;
                 g[r] = __ldcs(reinterpret_cast<const float4*>(a.log_alpha + at));
-                k[r] = *reinterpret_cast<const Four*>((const T*)a.k + at);
+                k[r] = *reinterpret_cast<const Raw*>((const T*)a.k + at);
             }
 #pragma unroll
             for (int r = 0; r < kAhead; ++r) {
@@ -274,7 +286,7 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
 
         // 2. the walks: lane l of a group holds channels 4 (l + 8 m) .. + 3
         const int l8 = lane % 8;
-        float4 wk[kQuads], wq[kQuads];
+        F2 wk[kQuads][2], wq[kQuads][2];
         const int node = warp * 4 + lane / 8 < live ? sm.order[warp * 4 + lane / 8] : -1;
         {
             const int i = node;
@@ -283,16 +295,20 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
             if (i >= 0) {
                 j = sm.par[i];
                 place = sm.off[i];
+                F2 self = both(0.f);
 #pragma unroll
                 for (int m = 0; m < kQuads; ++m) {
                     const int c = 4 * (l8 + 8 * m);
                     const float4 q = load4((const T*)a.q + (tok0 + i * a.H) * DK + c);
-                    const float4 k = *reinterpret_cast<const float4*>(kf + i * DK + c);
-                    const float4 g = *reinterpret_cast<const float4*>(alpha + i * DK + c);
-                    dot.y += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-                    wk[m] = make_float4(k.x * g.x, k.y * g.y, k.z * g.z, k.w * g.w);
-                    wq[m] = make_float4(q.x * g.x, q.y * g.y, q.z * g.z, q.w * g.w);
+                    const Four k = four(kf + i * DK + c), g = four(alpha + i * DK + c);
+                    const F2 q0(q.x, q.y), q1(q.z, q.w);
+                    self = fma2(q1, k.b, fma2(q0, k.a, self));
+                    wk[m][0] = mul2(k.a, g.a);
+                    wk[m][1] = mul2(k.b, g.b);
+                    wq[m][0] = mul2(q0, g.a);
+                    wq[m][1] = mul2(q1, g.b);
                 }
+                dot.y = self.x() + self.y();
             }
             int at_node = i;                                   // the node whose dots are in `dot`
             // every lane of the warp goes round as often as its longest path asks
@@ -309,18 +325,19 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
                 ++place;
                 at_node = j;
                 if (j >= 0) {
-                    dot = make_float2(0.f, 0.f);
+                    F2 x = both(0.f), y = both(0.f);
 #pragma unroll
                     for (int m = 0; m < kQuads; ++m) {
                         const int c = 4 * (l8 + 8 * m);
-                        const float4 k = *reinterpret_cast<const float4*>(kf + j * DK + c);
-                        const float4 g = *reinterpret_cast<const float4*>(alpha + j * DK + c);
-                        float4 &x = wk[m], &y = wq[m];
-                        dot.x += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
-                        dot.y += y.x * k.x + y.y * k.y + y.z * k.z + y.w * k.w;
-                        x.x *= g.x; x.y *= g.y; x.z *= g.z; x.w *= g.w;
-                        y.x *= g.x; y.y *= g.y; y.z *= g.z; y.w *= g.w;
+                        const Four k = four(kf + j * DK + c), g = four(alpha + j * DK + c);
+                        x = fma2(wk[m][1], k.b, fma2(wk[m][0], k.a, x));
+                        y = fma2(wq[m][1], k.b, fma2(wq[m][0], k.a, y));
+                        wk[m][0] = mul2(wk[m][0], g.a);
+                        wk[m][1] = mul2(wk[m][1], g.b);
+                        wq[m][0] = mul2(wq[m][0], g.a);
+                        wq[m][1] = mul2(wq[m][1], g.b);
                     }
+                    dot = make_float2(x.x() + x.y(), y.x() + y.y());
                     j = sm.par[j];
                 }
             }
@@ -334,10 +351,10 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
                     for (int m = 0; m < kQuads; ++m)
 #pragma unroll
                         for (int which = 0; which < 2; ++which) {
-                            const float4 x = which ? wq[m] : wk[m];
+                            const F2 x = which ? wq[m][0] : wk[m][0], y = which ? wq[m][1] : wk[m][1];
                             uint32_t lo[NS], hi[NS];
-                            split<NS>(x.x, x.y, lo);
-                            split<NS>(x.z, x.w, hi);
+                            split<NS>(x.x(), x.y(), lo);
+                            split<NS>(y.x(), y.y(), hi);
                             const int c = 4 * (l8 + 8 * m);
                             const uint32_t to = c / 64 * (2 * KP * 128) + umma::sw128_offset(which * KP + node, c % 64);
 #pragma unroll
