@@ -164,20 +164,22 @@ __device__ __forceinline__ int64_t glr_row(const GlrArgs& a, int64_t n, bool rep
     return s >= 0 && s < a.P ? s : -1;
 }
 
-// A tile in shared memory.  Aligned rows: kTile rows of kCh elements, lane l owns channels 2 l,
-// 2 l + 1.  Otherwise R boxes of kTile / R rows; lane l owns channels l, l + 32, and the offset
-// of a token's channel 0 is looked up (Stage::off).
-template <typename E, bool Aligned>
+// How rows lie.  kWhole: they start on 16 bytes; a tile is kTile rows of kCh elements.  Otherwise it is R
+// boxes of kTile / R rows, and the offset of a token's channel 0 is looked up (Stage::off).  Lane l owns
+// channels 2 l, 2 l + 1 as one access, or, where D is odd (kSingle), channels l, l + 32.  (bf16, 100000
+// tokens of 1024, 1022, 1023 channels: 168, 208, 232 us.)
+constexpr int kSingle = 0, kPairs = 1, kWhole = 2;
+template <typename E, int Mode>
 struct Rows {
     static constexpr int kBytes = kCh * (int)sizeof(E);
-    static constexpr int kPitch = kBytes + (Aligned ? 0 : 16);
+    static constexpr int kPitch = kBytes + (Mode == kWhole ? 0 : 16);
     static constexpr int kPer16 = 16 / (int)sizeof(E);
 
     // The lane's two channels of the row at `at` bytes.
     static __device__ __forceinline__ F2 get(const unsigned char* base, int at, int lane)
     {
         const E* p = reinterpret_cast<const E*>(base + at);
-        if constexpr (!Aligned) return F2(IO<E>::load(p, lane), IO<E>::load(p, lane + 32));
+        if constexpr (Mode == kSingle) return F2(IO<E>::load(p, lane), IO<E>::load(p, lane + 32));
         if constexpr (sizeof(E) == 4) {
             F2 v;
             v.v = reinterpret_cast<const unsigned long long*>(p)[lane];
@@ -191,7 +193,7 @@ struct Rows {
     {
         static_assert(sizeof(E) == 4, "decays only");
         float* p = reinterpret_cast<float*>(base + at);
-        if constexpr (Aligned) {
+        if constexpr (Mode != kSingle) {
             reinterpret_cast<unsigned long long*>(p)[lane] = v.v;
         } else {
             p[lane] = v.x();
@@ -201,16 +203,16 @@ struct Rows {
     // The same from the tensor itself.
     static __device__ __forceinline__ F2 direct(const E* at, bool on0, bool on1)
     {
-        return F2(on0 ? IO<E>::load(at, 0) : 0.f, on1 ? IO<E>::load(at, Aligned ? 1 : 32) : 0.f);
+        return F2(on0 ? IO<E>::load(at, 0) : 0.f, on1 ? IO<E>::load(at, Mode != kSingle ? 1 : 32) : 0.f);
     }
 };
 
 // The lane's two channels, from c0, of a row of a tensor in global memory; on0, on1: which of
-// them exist (aligned: both or none).
-template <typename E, bool Aligned>
+// them exist (of a pair both or none).
+template <typename E, int Mode>
 __device__ __forceinline__ void store_pair(E* at, bool on0, bool on1, F2 v)
 {
-    if constexpr (Aligned) {
+    if constexpr (Mode != kSingle) {
         if (!on0) return;
         if constexpr (sizeof(E) == 4) {
             __stcs(reinterpret_cast<float2*>(at), make_float2(v.x(), v.y()));
@@ -223,10 +225,10 @@ __device__ __forceinline__ void store_pair(E* at, bool on0, bool on1, F2 v)
         if (on1) IO<E>::store(at, 32, v.y());
     }
 }
-template <bool Aligned>
+template <int Mode>
 __device__ __forceinline__ F2 load_pair(const float* at, bool on0, bool on1)
 {
-    return F2(at && on0 ? at[0] : 0.f, at && on1 ? at[Aligned ? 1 : 32] : 0.f);
+    return F2(at && on0 ? at[0] : 0.f, at && on1 ? at[Mode != kSingle ? 1 : 32] : 0.f);
 }
 
 // Tokens of a row that are in a sequence: with cu_seqlens (one row) those behind the last sequence
@@ -239,10 +241,10 @@ __device__ __forceinline__ int64_t tokens_used(const GlrArgs& a)
 }
 
 // One stage of the ring.
-template <typename T, bool Aligned, bool Bwd>
+template <typename T, int Mode, bool Bwd>
 struct Stage {
-    using La = Rows<float, Aligned>;
-    using X = Rows<T, Aligned>;
+    using La = Rows<float, Mode>;
+    using X = Rows<T, Mode>;
     alignas(128) unsigned char la[kTile * La::kPitch];           // log_a, then exp(log_a)
     alignas(128) unsigned char x[kTile * X::kPitch];
     alignas(128) unsigned char y[Bwd ? kTile * X::kPitch : 128]; // dout
@@ -250,7 +252,7 @@ struct Stage {
     float fA[Bwd ? kRuns : 1][kCh], fB[Bwd ? kRuns : 1][kCh];    // backward: the forward runs too
     float tA[kCh], tB[kCh], carry[kCh];                          // the tile; what enters it
     int first[kTile], last[kTile];                               // sequences that begin / end there, or -1
-    int off[Aligned ? 1 : kTile];                                // bytes of a token's channel 0: la | x << 16
+    int off[Mode == kWhole ? 1 : kTile];                                // bytes of a token's channel 0: la | x << 16
     int64_t id;                                                  // tile * cols + column; -1: no more
     int marked;                                                  // whether first / last hold anything
     int plain;                                                   // no marks, all tokens there and in the maps
@@ -258,12 +260,12 @@ struct Stage {
     uint64_t taken, full, agg, carried, empty;
     static constexpr uint32_t kCopied = kTile * (La::kPitch + X::kPitch * (Bwd ? 2 : 1));
 
-    __device__ __forceinline__ int la_at(int r) const { return Aligned ? r * La::kPitch : off[r] & 0xffff; }
-    __device__ __forceinline__ int x_at(int r) const { return Aligned ? r * X::kPitch : (int)((uint32_t)off[r] >> 16); }
+    __device__ __forceinline__ int la_at(int r) const { return Mode == kWhole ? r * La::kPitch : off[r] & 0xffff; }
+    __device__ __forceinline__ int x_at(int r) const { return Mode == kWhole ? r * X::kPitch : (int)((uint32_t)off[r] >> 16); }
 };
-template <typename T, bool Aligned, bool Bwd> constexpr int ring_stages()
+template <typename T, int Mode, bool Bwd> constexpr int ring_stages()
 {
-    constexpr int n = (int)((227 * 1024 - 64) / sizeof(Stage<T, Aligned, Bwd>));
+    constexpr int n = (int)((227 * 1024 - 64) / sizeof(Stage<T, Mode, Bwd>));
     return n < 8 ? n : 8;
 }
 
@@ -328,19 +330,19 @@ __global__ void __launch_bounds__(256) glr_setup_kernel(GlrArgs a, ScanWork w, i
     }
 }
 
-// Tensor maps of log_a, x and dout (aligned rows).
+// Tensor maps of log_a, x and dout.
 struct ScanMaps {
     CUtensorMap la, x, y;
 };
 
 // The loader: one warp.
-template <typename T, bool Aligned, bool Bwd, int NS>
+template <typename T, int Mode, bool Bwd, int NS>
 __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, const ScanMaps& maps,
-                                          Stage<T, Aligned, Bwd>* ring)
+                                          Stage<T, Mode, Bwd>* ring)
 {
-    using S = Stage<T, Aligned, Bwd>;
+    using S = Stage<T, Mode, Bwd>;
     const int lane = threadIdx.x % 32;
-    const int R = Aligned ? 1 : 1 << w.log_r;
+    const int R = Mode == kWhole ? 1 : 1 << w.log_r;
     const int64_t used = tokens_used(a);
     int64_t next = blockIdx.x;
     int ends = 0;
@@ -367,19 +369,19 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
         __syncwarp();
         if (copies && lane < R) {
             // the box of tokens whose index over all rows is `lane` modulo R
-            const int64_t row = (at.row0 - lane + R - 1) >> (Aligned ? 0 : w.log_r);
+            const int64_t row = (at.row0 - lane + R - 1) >> (Mode == kWhole ? 0 : w.log_r);
             const int64_t x0 = lane * a.D + at.c0;
             const int box = kTile / R;
             const int32_t xa = (int32_t)(x0 & ~(int64_t)(S::La::kPer16 - 1)), xx = (int32_t)(x0 & ~(int64_t)(S::X::kPer16 - 1));
-            tma::load_2d(s.la + lane * box * S::La::kPitch, &maps.la, Aligned ? (int32_t)x0 : xa, (int32_t)row, &s.full);
-            tma::load_2d(s.x + lane * box * S::X::kPitch, &maps.x, Aligned ? (int32_t)x0 : xx, (int32_t)row, &s.full);
+            tma::load_2d(s.la + lane * box * S::La::kPitch, &maps.la, Mode == kWhole ? (int32_t)x0 : xa, (int32_t)row, &s.full);
+            tma::load_2d(s.x + lane * box * S::X::kPitch, &maps.x, Mode == kWhole ? (int32_t)x0 : xx, (int32_t)row, &s.full);
             if constexpr (Bwd)
-                tma::load_2d(s.y + lane * box * S::X::kPitch, &maps.y, Aligned ? (int32_t)x0 : xx, (int32_t)row, &s.full);
+                tma::load_2d(s.y + lane * box * S::X::kPitch, &maps.y, Mode == kWhole ? (int32_t)x0 : xx, (int32_t)row, &s.full);
         }
         if (id < 0) {
             ++ends;                              // one for every worker that takes tiles in turn
         } else {
-            if constexpr (!Aligned)
+            if constexpr (Mode != kWhole)
                 for (int r = lane; r < kTile; r += 32) {
                     const int place = (int)((at.row0 + r) & (R - 1));
                     const int slot = place * (kTile >> w.log_r) + (r >> w.log_r);
@@ -413,11 +415,11 @@ __device__ __forceinline__ void scan_load(const GlrArgs& a, const ScanWork& w, c
 }
 
 // An aggregator warp: run `run` of one tile of agg_groups(Bwd), from tile `group` on.
-template <typename T, bool Aligned, bool Bwd, int NS>
-__device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring,
+template <typename T, int Mode, bool Bwd, int NS>
+__device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork& w, Stage<T, Mode, Bwd>* ring,
                                                int group, int run)
 {
-    using S = Stage<T, Aligned, Bwd>;
+    using S = Stage<T, Mode, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
     const int64_t used = tokens_used(a);
     for (int64_t q = group;; q += agg_groups(Bwd)) {
@@ -445,8 +447,8 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
             }
         } else {
             const int live = (int)(used - at.t0 < kTile ? used - at.t0 : kTile);   // tokens that exist (or less than none)
-            const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
-            const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
+            const int64_t c = at.c0 + (Mode != kSingle ? 2 * lane : lane);
+            const bool on0 = c < a.D, on1 = c + (Mode != kSingle ? 1 : 32) < a.D;
             for (int r = r0; r < r0 + kSteps && r < live; ++r) {
                 const bool in = at.row0 + r < w.mapped;
                 const int64_t e = (at.row0 + r) * a.D + c;
@@ -455,14 +457,14 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
                 const int n = s.marked ? s.first[r] : -1;
                 if (n >= 0) {
                     const int64_t row = Bwd ? n : glr_row(a, n, lane == 0 && at.c0 == 0);
-                    const F2 h0 = load_pair<Aligned>(a.h0 && row >= 0 ? a.h0 + row * a.D + c : nullptr, on0, on1);
+                    const F2 h0 = load_pair<Mode>(a.h0 && row >= 0 ? a.h0 + row * a.D + c : nullptr, on0, on1);
                     A = F2(-1.f, -1.f);
                     B = add2(mul2(l, h0), x);
                     if constexpr (!Bwd) {
                         // the finishers find exp(log_a) h0 here: hT may be written over h0 before they come
                         l = mul2(l, h0);
                         if (a.starts && r == 0)
-                            store_pair<float, Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, h0);
+                            store_pair<float, Mode>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, h0);
                     }
                 } else {
                     A = mul2(A, l);
@@ -479,7 +481,7 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
                     const int n = s.marked ? s.last[r] : -1;
                     if (n >= 0) {
                         A = F2(-1.f, -1.f);
-                        B = load_pair<Aligned>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
+                        B = load_pair<Mode>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
                     }
                     const F2 l = S::La::get(s.la, s.la_at(r), lane);
                     const F2 y = at.row0 + r < w.mapped
@@ -559,10 +561,10 @@ __device__ __forceinline__ void append(float (&A)[2], float (&B)[2], unsigned lo
 }
 
 // A carrier warp: one tile of carry_warps(NS), from tile `from` on.
-template <typename T, bool Aligned, bool Bwd, int NS>
-__device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring, int from)
+template <typename T, int Mode, bool Bwd, int NS>
+__device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, Stage<T, Mode, Bwd>* ring, int from)
 {
-    using S = Stage<T, Aligned, Bwd>;
+    using S = Stage<T, Mode, Bwd>;
     const int lane = threadIdx.x % 32;
     for (int64_t q = from;; q += carry_warps(NS)) {
         S& s = ring[q % NS];
@@ -623,11 +625,11 @@ __device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, 
 }
 
 // A finisher warp: run `run` of one tile of kFinGroups, from tile `group` on.
-template <typename T, bool Aligned, bool Bwd, int NS>
-__device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w, Stage<T, Aligned, Bwd>* ring,
+template <typename T, int Mode, bool Bwd, int NS>
+__device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w, Stage<T, Mode, Bwd>* ring,
                                             int group, int run)
 {
-    using S = Stage<T, Aligned, Bwd>;
+    using S = Stage<T, Mode, Bwd>;
     const int lane = threadIdx.x % 32, r0 = run * kSteps;
     const int64_t used = tokens_used(a);
     for (int64_t q = group;; q += kFinGroups) {
@@ -635,10 +637,10 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
         if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
         const TileAt at(a, w, s.id, Bwd);
         const int live = (int)(used - at.t0 < kTile ? used - at.t0 : kTile);     // tokens that exist (or less than none)
-        const int64_t c = at.c0 + (Aligned ? 2 * lane : lane);
-        const bool on0 = c < a.D, on1 = c + (Aligned ? 1 : 32) < a.D;
+        const int64_t c = at.c0 + (Mode != kSingle ? 2 * lane : lane);
+        const bool on0 = c < a.D, on1 = c + (Mode != kSingle ? 1 : 32) < a.D;
         F2 enter(0.f, 0.f);                      // backward: the kept entry state, asked for before the wait
-        if constexpr (Bwd) enter = load_pair<Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1);
+        if constexpr (Bwd) enter = load_pair<Mode>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1);
         if (!umma::mbar_wait(&s.carried, (uint32_t)((q / NS) & 1), a.err, kScanBit)) return;
         const bool marked = s.marked != 0;
         // x or dout of a token
@@ -655,23 +657,23 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
                 for (int e = 0; e < 2; ++e) h[e] = leave(s.A[k][2 * lane + e], s.B[k][2 * lane + e], h[e]);
             F2 H(h[0], h[1]);
             if (a.starts && run == 0 && !(marked && s.first[0] >= 0))
-                store_pair<float, Aligned>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, H);
+                store_pair<float, Mode>(a.starts + (at.b * w.tiles + at.i) * a.D + c, on0, on1, H);
             T* out = (T*)a.out + (at.row0 + r0) * a.D + c;
             if (s.plain && a.out) {
 #pragma unroll 4
                 for (int r = r0; r < r0 + kSteps; ++r, out += a.D) {
                     H = fma2(S::La::get(s.la, s.la_at(r), lane), H, S::X::get(s.x, s.x_at(r), lane));
-                    store_pair<T, Aligned>(out, on0, on1, H);
+                    store_pair<T, Mode>(out, on0, on1, H);
                 }
             } else {
                 for (int r = r0; r < live && r < r0 + kSteps; ++r, out += a.D) {
                     const F2 l = S::La::get(s.la, s.la_at(r), lane), x = value(s.x, a.x, r);
                     H = marked && s.first[r] >= 0 ? add2(l, x) : fma2(l, H, x);
-                    if (a.out) store_pair<T, Aligned>(out, on0, on1, H);
+                    if (a.out) store_pair<T, Mode>(out, on0, on1, H);
                     const int n = marked && a.hT ? s.last[r] : -1;
                     if (n >= 0) {
                         const int64_t row = glr_row(a, n, false);
-                        if (row >= 0) store_pair<float, Aligned>(a.hT + row * a.D + c, on0, on1, H);
+                        if (row >= 0) store_pair<float, Mode>(a.hT + row * a.D + c, on0, on1, H);
                     }
                 }
             }
@@ -699,9 +701,9 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
 #pragma unroll
                 for (int k = kSteps - 1; k >= 0; --k, to -= a.D, ta -= a.D) {
                     G = add2(G, S::X::get(s.y, s.x_at(r0 + k), lane));
-                    store_pair<T, Aligned>(to, on0, on1, G);
+                    store_pair<T, Mode>(to, on0, on1, G);
                     G = mul2(G, S::La::get(s.la, s.la_at(r0 + k), lane));
-                    store_pair<float, Aligned>(ta, on0, on1, mul2(G, before[k]));
+                    store_pair<float, Mode>(ta, on0, on1, mul2(G, before[k]));
                 }
             } else {
 #pragma unroll
@@ -710,7 +712,7 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
                     if (r >= live) break;
                     const int n = marked ? s.first[r] : -1;
                     if (n >= 0)
-                        H = load_pair<Aligned>(a.h0 ? a.h0 + (int64_t)n * a.D + c : nullptr, on0, on1);
+                        H = load_pair<Mode>(a.h0 ? a.h0 + (int64_t)n * a.D + c : nullptr, on0, on1);
                     before[k] = H;
                     H = fma2(S::La::get(s.la, s.la_at(r), lane), H, value(s.x, a.x, r));
                 }
@@ -720,14 +722,14 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
                     if (r >= live) continue;
                     const int n = marked ? s.last[r] : -1;
                     if (n >= 0)
-                        G = load_pair<Aligned>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
+                        G = load_pair<Mode>(a.dhT ? a.dhT + (int64_t)n * a.D + c : nullptr, on0, on1);
                     G = add2(G, value(s.y, a.dout, r));
                     const int64_t to = (at.row0 + r) * a.D + c;
-                    store_pair<T, Aligned>((T*)a.dx + to, on0, on1, G);
+                    store_pair<T, Mode>((T*)a.dx + to, on0, on1, G);
                     G = mul2(G, S::La::get(s.la, s.la_at(r), lane));
-                    store_pair<float, Aligned>(a.dlog_a + to, on0, on1, mul2(G, before[k]));
+                    store_pair<float, Mode>(a.dlog_a + to, on0, on1, mul2(G, before[k]));
                     const int m = marked && a.dh0 ? s.first[r] : -1;
-                    if (m >= 0) store_pair<float, Aligned>(a.dh0 + (int64_t)m * a.D + c, on0, on1, G);
+                    if (m >= 0) store_pair<float, Mode>(a.dh0 + (int64_t)m * a.D + c, on0, on1, G);
                 }
             }
         }
@@ -736,13 +738,13 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
     }
 }
 
-template <typename T, bool Aligned, bool Bwd>
-__global__ void __launch_bounds__(scan_threads(ring_stages<T, Aligned, Bwd>(), Bwd), 1)
+template <typename T, int Mode, bool Bwd>
+__global__ void __launch_bounds__(scan_threads(ring_stages<T, Mode, Bwd>(), Bwd), 1)
 glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
 {
     griddep_wait();
-    using S = Stage<T, Aligned, Bwd>;
-    constexpr int NS = ring_stages<T, Aligned, Bwd>();
+    using S = Stage<T, Mode, Bwd>;
+    constexpr int NS = ring_stages<T, Mode, Bwd>();
     static_assert(NS > agg_groups(Bwd) && NS > kFinGroups, "every group meets an end, and ends take a stage each");
     extern __shared__ __align__(128) unsigned char smem[];
     S* ring = reinterpret_cast<S*>(smem);
@@ -758,12 +760,12 @@ glr_scan_kernel(GlrArgs a, ScanWork w, const __grid_constant__ ScanMaps maps)
     }
     __syncthreads();
     constexpr int kAggWarps = agg_groups(Bwd) * kRuns;
-    if (warp < kAggWarps) return scan_aggregate<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
+    if (warp < kAggWarps) return scan_aggregate<T, Mode, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
     warp -= kAggWarps;
-    if (warp < kFinWarps) return scan_finish<T, Aligned, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
+    if (warp < kFinWarps) return scan_finish<T, Mode, Bwd, NS>(a, w, ring, warp / kRuns, warp % kRuns);
     warp -= kFinWarps;
-    if (warp < carry_warps(NS)) return scan_carry<T, Aligned, Bwd, NS>(a, w, ring, warp);
-    scan_load<T, Aligned, Bwd, NS>(a, w, maps, ring);
+    if (warp < carry_warps(NS)) return scan_carry<T, Mode, Bwd, NS>(a, w, ring, warp);
+    scan_load<T, Mode, Bwd, NS>(a, w, maps, ring);
 }
 
 // One token per sequence: read and written once, V channels a thread (one access each where rows
@@ -811,7 +813,7 @@ glr_step_kernel(const T* __restrict__ x, const float* __restrict__ log_a, float*
 
 namespace {
 
-template <typename T, bool Aligned, bool Bwd>
+template <typename T, int Mode, bool Bwd>
 cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
 {
     ScanWork w = {};
@@ -841,18 +843,18 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
         if (s != cudaSuccess) return s;
     }
     if (w.total == 0) return cudaSuccess;
-    constexpr int smem = ring_stages<T, Aligned, Bwd>() * (int)sizeof(Stage<T, Aligned, Bwd>);
-    const auto kernel = glr_scan_kernel<T, Aligned, Bwd>;
+    constexpr int smem = ring_stages<T, Mode, Bwd>() * (int)sizeof(Stage<T, Mode, Bwd>);
+    const auto kernel = glr_scan_kernel<T, Mode, Bwd>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // rows of R tokens have a stride of 16 bytes
     constexpr bool bf16 = sizeof(T) == 2;
-    if (!Aligned) w.log_r = a.D * (int64_t)sizeof(T) % 8 == 0 ? 1 : a.D * (int64_t)sizeof(T) % 4 == 0 ? 2 : 3;
+    if (Mode != kWhole) w.log_r = a.D * (int64_t)sizeof(T) % 8 == 0 ? 1 : a.D * (int64_t)sizeof(T) % 4 == 0 ? 2 : 3;
     const int64_t R = int64_t(1) << w.log_r, rows = a.B * a.T / R;
     w.mapped = rows * R;
     ScanMaps maps = {};
     if (rows > 0) {
-        using S = Stage<T, Aligned, Bwd>;
+        using S = Stage<T, Mode, Bwd>;
         const auto map = [&](CUtensorMap* m, const void* p, bool half, int pitch) {
             const int e = half ? 2 : 4;
             return make_tensor_map_2d(m, p, half, (uint64_t)(R * a.D), (uint64_t)rows, (uint64_t)(R * a.D * e),
@@ -865,17 +867,22 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
     }
     LaunchScope scope(st, Bwd ? K_GLR_BWD : K_GLR_FWD);
     const int64_t sms = device_sm_count();
-    const dim3 grid((unsigned)(w.total < sms ? w.total : sms)), block(scan_threads(ring_stages<T, Aligned, Bwd>(), Bwd));
-    if (w.tiles == 1) return launch_pdl(glr_scan_kernel<T, Aligned, Bwd>, grid, block, smem, st, a, w, maps);
+    const dim3 grid((unsigned)(w.total < sms ? w.total : sms)), block(scan_threads(ring_stages<T, Mode, Bwd>(), Bwd));
+    if (w.tiles == 1) return launch_pdl(glr_scan_kernel<T, Mode, Bwd>, grid, block, smem, st, a, w, maps);
     return launch_coop(kernel, grid, block, smem, st, a, w, maps);
+}
+
+template <typename T, bool Bwd>
+cudaError_t launch_scan_io(const GlrArgs& a, cudaStream_t st)
+{
+    if (a.D * (int64_t)sizeof(T) % 16 == 0) return launch_scan<T, kWhole, Bwd>(a, st);
+    return a.D % 2 == 0 ? launch_scan<T, kPairs, Bwd>(a, st) : launch_scan<T, kSingle, Bwd>(a, st);
 }
 
 template <bool Bwd>
 cudaError_t launch_scan_t(const GlrArgs& a, cudaStream_t st)
 {
-    if (a.io == KDA_IO_F32)
-        return a.D % 4 == 0 ? launch_scan<float, true, Bwd>(a, st) : launch_scan<float, false, Bwd>(a, st);
-    return a.D % 8 == 0 ? launch_scan<__nv_bfloat16, true, Bwd>(a, st) : launch_scan<__nv_bfloat16, false, Bwd>(a, st);
+    return a.io == KDA_IO_F32 ? launch_scan_io<float, Bwd>(a, st) : launch_scan_io<__nv_bfloat16, Bwd>(a, st);
 }
 
 }  // namespace
