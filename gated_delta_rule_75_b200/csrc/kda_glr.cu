@@ -950,17 +950,17 @@ kda_status_t glr_fwd_impl(const void* x, const float* log_a, const float* h0, vo
     if ((cu && !is_aligned(cu, 4)) || (slots && !is_aligned(slots, 4))) return KDA_ERR_INVALID_ARG;
     if (!optional_ok(h0) || !optional_ok(hT) || !optional_ok(starts)) return KDA_ERR_INVALID_ARG;
     const int64_t rows = cu ? 1 : B, n = rows * T * D, e = io == KDA_IO_F32 ? 4 : 2;
+    const int64_t nh = (slots ? P : B) * D * 4;
     if (n > 0) {
         if (!tensor_ok(x) || !tensor_ok(log_a) || !tensor_ok(out)) return KDA_ERR_INVALID_ARG;
         const int64_t ns = rows * ((T + KDA_GLR_TILE - 1) / KDA_GLR_TILE) * D * 4;
-        const int64_t nh = (slots ? P : B) * D * 4;
         if (overlap(out, n * e, x, n * e) || overlap(out, n * e, log_a, n * 4) ||
             overlap(out, n * e, h0, nh) || overlap(out, n * e, hT, nh) || overlap(out, n * e, starts, ns) ||
             overlap(hT, nh, x, n * e) || overlap(hT, nh, log_a, n * 4) || overlap(hT, nh, starts, ns) ||
             overlap(starts, ns, x, n * e) || overlap(starts, ns, log_a, n * 4) || overlap(starts, ns, h0, nh))
             return KDA_ERR_INVALID_ARG;
-        if (hT != h0 && overlap(hT, nh, h0, nh)) return KDA_ERR_INVALID_ARG;
     }
+    if (hT != h0 && overlap(hT, nh, h0, nh)) return KDA_ERR_INVALID_ARG;     // without tokens too: hT = h0 then
     GlrArgs a = {};
     a.x = x; a.log_a = log_a; a.h0 = h0; a.hT = hT; a.out = out; a.starts = starts;
     a.slots = slots; a.P = P; a.cu = cu; a.N = B; a.B = rows; a.T = T; a.D = D; a.io = io;
@@ -1041,6 +1041,7 @@ kda_status_t kda_glr_scan_bwd(const void* x, const float* log_a, const float* h0
                 if (overlap(res[i].p, res[i].n, res[j].p, res[j].n)) return KDA_ERR_INVALID_ARG;
         }
     }
+    if (overlap(dh0, nh, dhT, nh)) return KDA_ERR_INVALID_ARG;               // without tokens dh0 = dhT
     GlrArgs a = {};
     a.x = x; a.log_a = log_a; a.h0 = h0; a.starts = const_cast<float*>(starts);
     a.dout = dout; a.dhT = dhT; a.dx = dx; a.dlog_a = dlog_a; a.dh0 = dh0;

@@ -17,7 +17,7 @@
 // steps: 18,700 (24,500) cycles, of which 4,700 are loads, 4,500 (3,900) the products and 3,100
 // (6,300) the levels; three CTAs of an SM cover one another up to 16 nodes, two up to 32, and the
 // state of the CTA that follows is brought into the L2 meanwhile.  64 x 16 nodes, 32 heads: 58 us, 3.2 TB/s
-// (two CTAs, all of S0 at once: 72); 40 x 61 nodes: 126 us.
+// (two CTAs, all of S0 at once: 72); 40 x 61 nodes: 125 us.
 // One CTA for one (sequence, head).  The walking warps, eight lanes a node:
 //   1. alpha, k into shared memory; depths, order by depth;
 //   2. walk up the node's path, every lane 16 (8) channels: the dots with every ancestor (three

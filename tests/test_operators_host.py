@@ -54,6 +54,7 @@ def test_scan_argument_errors(lib):
     assert scan(lib, out=at(0)) == BAD and scan(lib, out=at(1, 1024)) == BAD          # over x, inside log_a
     assert scan(lib, hT=at(2, 64)) == BAD and scan(lib, starts=at(2)) == BAD
     assert scan(lib, h0=at(3), hT=at(3, 256)) == BAD                                   # half over h0
+    assert scan(lib, T=0, h0=at(3), hT=at(3, 256)) == BAD                              # without tokens too
     assert scan(lib, B=0) == OK and scan(lib, D=0) == OK
     assert lib.kda_glr_scan_fwd_slots(at(0), at(1), at(2), None, at(3), None, None, 2, 100, 4, 64, 1, None) == BAD
     assert lib.kda_glr_scan_fwd_slots(at(0), at(1), None, at(4), at(3), None, None, 2, 100, 4, 64, 1, None) == BAD
@@ -69,6 +70,7 @@ def test_scan_backward_argument_errors(lib):
     assert scan_bwd(lib, dx=at(3)) == BAD and scan_bwd(lib, dg=at(1)) == BAD and scan_bwd(lib, dx=at(5)) == BAD
     assert scan_bwd(lib, dh0=at(6, 4)) == BAD and scan_bwd(lib, dh0=at(4)) == BAD
     assert scan_bwd(lib, dhT=at(6), dh0=at(6, 128)) == BAD and scan_bwd(lib, dhT=at(6), dh0=at(6)) == BAD
+    assert scan_bwd(lib, T=0, dhT=at(6), dh0=at(6, 128)) == BAD
     assert scan_bwd(lib, cu=at(6), B=0) == BAD and scan_bwd(lib, B=0) == OK
 
 
