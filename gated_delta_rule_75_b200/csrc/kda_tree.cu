@@ -136,7 +136,16 @@ template <int KB> __device__ __forceinline__ void walkers_sync()
 {
     asm volatile("bar.sync 1, %0;" ::"n"(tree_walkers(KB)) : "memory");
 }
-__device__ __forceinline__ void stagers_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kTreeStagers) : "memory"); }
+// Whether all staging threads say so.
+__device__ __forceinline__ bool stagers_all(bool ok)
+{
+    int all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 2, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all)
+                 : "r"((int)ok), "n"(kTreeStagers)
+                 : "memory");
+    return all != 0;
+}
 
 template <typename T, int DK, int DV, int KB>
 __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(KB, sizeof(T))) tree_fwd_kernel(const TreeArgs a)
@@ -371,14 +380,16 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
     if (S0) {
         if (tid == 0) multiply(0);
         if (Smem::kPieces > 1 && warp >= kStageWarp) {
-            umma::mbar_wait(&sm.done[0], 0, a.err, kTreeErrBit);
-            for (int k0 = 0; k0 < Smem::kRows; k0 += kLoads * kStep) {
+            // the first piece's products, another thread's, have read their operands and come before the second's
+            // in the sums; if they do not end, the second piece is left out and so is its signal
+            const bool first = __all_sync(0xffffffffu, umma::mbar_wait(&sm.done[0], 0, a.err, kTreeErrBit));
+            umma::fence_after_sync();
+            for (int k0 = 0; first && k0 < Smem::kRows; k0 += kLoads * kStep) {
                 if (k0 > 0) ask(1, k0);
                 put(k0);
             }
             umma::fence_smem_to_async();
-            stagers_sync();
-            if (tid == kWalkers) multiply(1);
+            if (stagers_all(first) && tid == kWalkers) multiply(1);
         }
     }
     // a thread's column and its first 16 rows: v is asked for before the wait.  Lane = column of S0,

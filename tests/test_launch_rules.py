@@ -76,3 +76,45 @@ def test_rule_check_catches_a_late_wait():
     assert _first_statement(srcs, "bad_kernel") == "int v = *p"
     srcs["x.cu"] = srcs["x.cu"].replace("{\n    int v", "{\n    constexpr int n = 4;\n    int v")
     assert _first_statement(srcs, "bad_kernel") == "int v = *p"
+
+
+def _waits_without_order(code):
+    """Waits for tensor-core products (on a barrier that a commit() arrives on) after which the function
+    goes on without looking at the outcome, or issues products, reads or writes tensor memory, or ends
+    its tensor-memory part without fence_after_sync()."""
+    code = _strip_comments(code)
+    bars = {m.group(1) for m in re.finditer(r"\bcommit\(&([\w.]+)", code)}
+    bad = []
+    for m in re.finditer(r"\b(?:mbar_wait|mbar_wait_spin|block_wait)\(&([\w.]+)[^;]*;", code):
+        if m.group(1) not in bars or "nullptr" in m.group(0):     # nullptr: the drain of a kernel that gave up
+            continue
+        start = max(code.rfind(c, 0, m.start()) for c in ";{}") + 1
+        statement = code[start:m.end()].strip()
+        if re.match(r"(?:\w+::)*(?:mbar_wait|mbar_wait_spin|block_wait)\(", statement):
+            bad.append("outcome not looked at: " + statement)
+        after = re.search(r"fence_after_sync\(|mma_bf16\(|multiply\(|tmem_ld|tmem_st|commit\(", code[m.end():])
+        if after is None or after.group(0) != "fence_after_sync(":
+            bad.append("no fence: " + statement)
+    return bad
+
+
+def test_waits_for_tensor_core_products_are_ordered():
+    """A thread that follows another's tcgen05 products (the drafted trees' second piece follows the first
+    into the same sums and overwrites its operand) takes up tcgen05 work again only behind
+    fence_after_sync(), and only if its bounded wait ended well."""
+    assert _waits_without_order(_sources()["kda_tree.cu"]) == []
+
+
+def test_rule_check_catches_an_unordered_wait():
+    planted = """
+        umma::commit(&sm.done[piece]);
+        umma::mbar_wait(&sm.done[0], 0, a.err, kBit);
+        put(0);
+        stagers_sync();
+        multiply(1);
+    """
+    found = _waits_without_order(planted)
+    assert len(found) == 2 and found[0].startswith("outcome") and found[1].startswith("no fence")
+    mended = planted.replace("umma::mbar_wait(&sm.done[0], 0, a.err, kBit);",
+                             "const bool ok = umma::mbar_wait(&sm.done[0], 0, a.err, kBit);\n umma::fence_after_sync();")
+    assert _waits_without_order(mended) == []
