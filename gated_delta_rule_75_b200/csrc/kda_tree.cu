@@ -14,10 +14,10 @@
 // A head's state is 64 KiB at d = 128, its 16 drafted tokens 24 KiB: 2 us of an SM's share of the
 // memory, next to 1 MFLOP of products with S0 (4 for 64 nodes), which mma.sync took 1.6 (6.5) us of
 // an SM for, so they are on tcgen05: 0.3 (0.8) us.  What bounds the kernel is the latency of its
-// steps: 18,700 (24,500) cycles, of which 4,700 are loads, 4,500 (3,900) the products and 3,100
-// (6,300) the levels; three CTAs of an SM cover one another up to 16 nodes, two up to 32, and the
-// state of the CTA that follows is brought into the L2 meanwhile.  64 x 16 nodes, 32 heads: 58 us, 3.2 TB/s
-// (two CTAs, all of S0 at once: 72); 40 x 61 nodes: 125 us.
+// steps: 20,600 (29,300) cycles, of which 5,100 (6,000) are loads, 5,400 (5,000) the products and 3,400
+// (8,000) the levels; three CTAs of an SM cover one another up to 16 nodes, two up to 32, and the
+// state of the CTA that follows is brought into the L2 meanwhile.  64 x 16 nodes, 32 heads: 68 us, 2.7 TB/s;
+// 40 x 61 nodes: 142 us.
 // One CTA for one (sequence, head).  The walking warps, eight lanes a node:
 //   1. alpha, k into shared memory; depths, order by depth;
 //   2. walk up the node's path, every lane 16 (8) channels: the dots with every ancestor (three
@@ -25,8 +25,11 @@
 //   3. the rows (keys, then queries) as bf16 summands in shared memory.
 // Meanwhile four more warps bring S0 there, as bf16 summands too.  Then one thread issues the
 // product, transposed, D^T = S0^T rows^T: M = dv, N = rows, so that N and the tensor memory follow
-// the number of nodes.  Rows and S0 are split into two bf16 summands each (three for fp32 I/O) and
-// the products down to 2^-17 (2^-25) of the whole are summed in fp32.  Then, all warps:
+// the number of nodes.  Rows and S0 are split into three bf16 summands each, which hold all 24 bits of
+// an fp32 value whatever the I/O type (two would take 59 and 125 us, and round the state to 17 bits).
+// Products down to 2^-16 of the largest are taken, those of a weight into sums of their own: an addition
+// in tensor memory truncates, and the sums that reach full size take 8 that way, not 48 (128 terms: 1.4e-7
+// off, 1.4e-6 with all in the same sums).  Then, all warps:
 //   4. D^T to shared memory; level by level, a warp a node: u_i and o_i.
 #include "kda_common.cuh"
 #include "kda_f32x2.cuh"
@@ -68,12 +71,12 @@ __device__ __forceinline__ Four four(const float* p)
     return f;
 }
 
-// (x, y) as NS bf16 pairs whose sum is within 2^-(8 NS + 1) of each: s[0] the largest.
-template <int NS>
-__device__ __forceinline__ void split(float x, float y, uint32_t (&s)[NS])
+// (x, y) as three bf16 pairs, the largest first, whose sum is x, y: each takes 8 of the 24 bits.
+constexpr int kSummands = 3;
+__device__ __forceinline__ void split(float x, float y, uint32_t (&s)[kSummands])
 {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < kSummands; ++i) {
         s[i] = pack_bf16(x, y);
         x -= __uint_as_float(s[i] << 16);
         y -= __uint_as_float(s[i] & 0xffff0000u);
@@ -88,11 +91,13 @@ constexpr int tree_per_sm(int KB, int io_bytes) { return KB == 64 ? 1 : KB == 32
 constexpr int kTreeErrBit = 2;                             // "operand MMAs" of the error word
 
 // Shared memory of a CTA for trees of up to KB nodes.
-template <int DK, int DV, int KB, int NS>
+template <int DK, int DV, int KB, int IoBytes>
 struct TreeSmem {
-    static constexpr int kPairs = KB * (KB + 1) / 2;
-    // S0 comes in one piece, or, where that lets a third CTA onto the SM, 64 rows at a time
-    static constexpr int kPieces = KB == 16 ? DK / 64 : 1, kRows = DK / kPieces;
+    static constexpr int NS = kSummands, kPairs = KB * (KB + 1) / 2;
+    // S0 comes in one piece, or, where that lets another CTA onto the SM, 64 rows at a time
+    static constexpr int kPieces = tree_per_sm(KB, IoBytes) > 1 ? DK / 64 : 1, kRows = DK / kPieces;
+    static constexpr int kColumns = KB == 16 ? 128 : KB == 32 ? 256 : 512;     // of tensor memory
+    static_assert(NS * 2 * KB <= kColumns, "sums of NS weights for the rows of keys and queries");
     static constexpr int kState = kRows * DV * 2;          // bytes of one summand of a piece
     // with dv = 64 the upper half of the M = 128 operand is whatever follows: its rows are not used
     static constexpr int kSlack = DV == 64 ? kRows * 128 : 0;
@@ -150,11 +155,10 @@ __device__ __forceinline__ bool stagers_all(bool ok)
 template <typename T, int DK, int DV, int KB>
 __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(KB, sizeof(T))) tree_fwd_kernel(const TreeArgs a)
 {
-    constexpr int NS = sizeof(T) == 2 ? 2 : 3;
-    using Smem = TreeSmem<DK, DV, KB, NS>;
+    constexpr int NS = kSummands;
+    using Smem = TreeSmem<DK, DV, KB, sizeof(T)>;
     constexpr int kQuads = DK / 32;                        // float4 channel groups of a lane in the walk
     constexpr int kWalkers = tree_walkers(KB), kThreads = kWalkers + kTreeStagers, kStageWarp = kWalkers / 32;
-    constexpr int kColumns = 2 * KB < 32 ? 32 : 2 * KB;    // of tensor memory
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     float* alpha = reinterpret_cast<float*>(sm.region);
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
     const int64_t tok0 = (n * K) * a.H + h;                // node i: tok0 + i * H
     const int KP = (live + 15) / 16 * 16;                  // rows of keys, and of queries
     if (warp == kStageWarp) {
-        umma::tmem_alloc(&sm.tmem, kColumns);
+        umma::tmem_alloc(&sm.tmem, Smem::kColumns);
         umma::tmem_relinquish();
     }
     if (tid == 0) {
@@ -202,29 +206,34 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             uint32_t lo[NS], hi[NS];
-            split<NS>(s[i].x, s[i].y, lo);
-            split<NS>(s[i].z, s[i].w, hi);
+            split(s[i].x, s[i].y, lo);
+            split(s[i].z, s[i].w, hi);
             const uint32_t to = sc / 64 * (Smem::kRows * 128) + umma::sw128_offset(k0 + sr + i * kStep, sc % 64);
 #pragma unroll
             for (int e = 0; e < NS; ++e)
                 *reinterpret_cast<uint2*>(sm.state + e * Smem::kState + to) = make_uint2(lo[e], hi[e]);
         }
     };
-    // the products with one piece, by one thread
+    // The products with one piece, by one thread.  Summand i of S0 times summand j of the rows goes into sums
+    // i + j, so the first sums, which alone reach full size, take only one addition for 16 channels; the rows'
+    // summands lie side by side, and one MMA takes all that a summand of S0 is multiplied by
     const auto multiply = [&](int piece) {
-        const uint32_t idesc = umma::make_idesc_bf16(128, 2 * KP, true, false);
         const uint64_t ad = umma::make_desc(umma::smem_u32(sm.state), Smem::kRows * 128, 1024);
         const uint64_t bd = umma::make_desc(umma::smem_u32(sm.region), 16, 1024);
-        const uint32_t block = 2 * KP * 128 / 16;          // of the rows' channels, in descriptor units
+        const uint32_t block = NS * 2 * KP * 128 / 16;     // 64 channels of the rows, in descriptor units
 #pragma unroll
-        for (int sa = 0; sa < NS; ++sa)                    // summand of S0, of the rows
+        for (int ks = 0; ks < Smem::kRows / 16; ++ks) {
+            const int step = piece * (Smem::kRows / 16) + ks;
 #pragma unroll
-            for (int sb = 0; sb < NS - sa; ++sb)
-#pragma unroll
-                for (int ks = 0; ks < Smem::kRows / 16; ++ks)
-                    umma::mma_bf16(sm.tmem, ad + (sa * Smem::kState + ks * 2048) / 16,
-                                   bd + (sb * (DK / 64) + piece * (Smem::kRows / 64) + ks / 4) * block + ks % 4 * 2, idesc,
-                                   piece + sa + sb + ks > 0);
+            for (int i = 0; i < NS; ++i) {
+                const uint64_t at = ad + (i * Smem::kState + ks * 2048) / 16, bt = bd + step / 4 * block + step % 4 * 2;
+                const int columns = (NS - i) * 2 * KP, most = columns > 256 ? 256 : columns;
+                umma::mma_bf16(sm.tmem + i * 2 * KP, at, bt, umma::make_idesc_bf16(128, most, true, false), step + i > 0);
+                if (KB == 64 && columns > most)
+                    umma::mma_bf16(sm.tmem + i * 2 * KP + most, at, bt + most * 128 / 16,
+                                   umma::make_idesc_bf16(128, columns - most, true, false), step + i > 0);
+            }
+        }
         umma::commit(&sm.done[piece]);
     };
     if (warp >= kStageWarp) {
@@ -362,13 +371,14 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
                         for (int which = 0; which < 2; ++which) {
                             const F2 x = which ? wq[m][0] : wk[m][0], y = which ? wq[m][1] : wk[m][1];
                             uint32_t lo[NS], hi[NS];
-                            split<NS>(x.x(), x.y(), lo);
-                            split<NS>(y.x(), y.y(), hi);
+                            split(x.x(), x.y(), lo);
+                            split(y.x(), y.y(), hi);
                             const int c = 4 * (l8 + 8 * m);
-                            const uint32_t to = c / 64 * (2 * KP * 128) + umma::sw128_offset(which * KP + node, c % 64);
+                            // (the rows of a summand are a multiple of 8, where the swizzle repeats)
+                            const uint32_t to = c / 64 * (NS * 2 * KP * 128) + umma::sw128_offset(which * KP + node, c % 64);
 #pragma unroll
                             for (int e = 0; e < NS; ++e)
-                                *reinterpret_cast<uint2*>(sm.region + e * (2 * KP * DK * 2) + to) = make_uint2(lo[e], hi[e]);
+                                *reinterpret_cast<uint2*>(sm.region + e * (2 * KP * 128) + to) = make_uint2(lo[e], hi[e]);
                         }
         }
     }
@@ -410,8 +420,15 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
         for (int c0 = warp / 4 * 16; c0 < 2 * KP; c0 += kThreads / 128 * 16) {
             float x[16] = {};
             if (S0) {
-                umma::tmem_ld16(sm.tmem + ((uint32_t)(warp % 4 * 32) << 16) + c0, x);
-                umma::tmem_wait_ld();
+                const uint32_t from = sm.tmem + ((uint32_t)(warp % 4 * 32) << 16) + c0;
+#pragma unroll
+                for (int i = NS - 1; i >= 0; --i) {        // the smallest sums first
+                    float y[16];
+                    umma::tmem_ld16(from + i * 2 * KP, y);
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] += y[e];
+                }
             }
             if (c0 < KP) {                                 // keys: v - S0^T (..)
                 if (c0 >= kThreads / 128 * 16) load_v(c0, v0);
@@ -426,7 +443,7 @@ __global__ void __launch_bounds__(tree_walkers(KB) + kTreeStagers, tree_per_sm(K
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    if (warp == kStageWarp) umma::tmem_dealloc(sm.tmem, kColumns);
+    if (warp == kStageWarp) umma::tmem_dealloc(sm.tmem, Smem::kColumns);
     if (!fine) return;
 
     // 4. level by level; a lane holds CPL columns
@@ -560,7 +577,7 @@ namespace {
 template <typename T, int DK, int DV, int KB>
 cudaError_t tree_fwd_kb(TreeArgs a, cudaStream_t st)
 {
-    constexpr int smem = (int)sizeof(TreeSmem<DK, DV, KB, sizeof(T) == 2 ? 2 : 3>);
+    constexpr int smem = (int)sizeof(TreeSmem<DK, DV, KB, sizeof(T)>);
     const cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T, DK, DV, KB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

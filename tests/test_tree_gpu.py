@@ -136,3 +136,44 @@ def test_not_a_number_stays_on_its_branch(kda):
     out = kda.tree_fwd(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], x["state"], i32([par]), scale)
     bad = (~torch.isfinite(out[0, :, 0])).any(-1).tolist()
     assert bad == [False, True, False, True, False, False]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,dk,dv", [(1, 128, 128), (16, 128, 64), (16, 64, 128), (17, 128, 128), (32, 64, 64), (61, 128, 128)])
+def test_outputs_come_from_every_bit_of_the_state(kda, K, dk, dv, io):
+    """Queries and keys that pick one row of the cached state, no decay: every product is exact, so the output
+    is that row (or, behind a write of strength 1/2 of a zero value, half of it), rounded once and exactly.
+    The state's values lie 2^-20 beside the middle between two bf16 values: what is lost of 24 bits shows."""
+    g = torch.Generator().manual_seed(K + dk + dv)
+    N, H = 3, 2
+    coarse = torch.randint(128, 256, (N, H, dk, dv), generator=g) / 128.0                 # bf16 values in [1, 2)
+    side = (torch.randint(0, 2, coarse.shape, generator=g) * 2 - 1) * 2.0 ** -20
+    sign = torch.randint(0, 2, coarse.shape, generator=g) * 2.0 - 1
+    state = (coarse + 2.0 ** -8 + side) * sign * 2.0 ** torch.randint(-9, 9, (N, H, dk, 1), generator=g)
+    assert bool((state.to(torch.float32).double() == state.double()).all())
+    pick = torch.randint(0, dk, (N, K, H), generator=g)
+    q = torch.nn.functional.one_hot(pick, dk).to(R.IO[io])
+    v, zero = torch.zeros(N, K, H, dv, dtype=R.IO[io]), torch.zeros(N, K, H, dk)
+    rows = torch.stack([torch.stack([state[n, h][pick[n, :, h]] for h in range(H)], 1) for n in range(N)])
+    for beta, share in ((0.0, 1.0), (0.5, 0.5)):
+        out = kda.tree_fwd(q.cuda(), q.cuda(), v.cuda(), zero.cuda(), torch.full((N, K, H), beta).cuda(),
+                           state.float().cuda(), i32([[-1] * K] * N), 1.0)
+        assert torch.equal(out.cpu(), (share * rows).to(R.IO[io])), beta
+
+
+@pytest.mark.parametrize("K", [3, 16, 30, 64])
+def test_products_with_the_state_sum_up_closely(kda, K):
+    """The products with the state alone (no decay, no writes), fp32.  Operands are three bf16 summands, and
+    products of a weight have sums of their own, so the sums that reach the result's size take 8 additions of
+    16 channels.  An addition loses at most a step, 2^-23, of what is there by then, which after j of the 8 is
+    sqrt(j / 8) of the result's norm: 5.8 2^-23 in all, 16 2^-31 in the sums a weight below; a half step,
+    2^-24, for joining the sums, for the scale and for the products that are left out: under 8.8e-7, in any
+    rounding.  (All 48 additions at full size: up to 48 2^-23.)"""
+    x, scale = R.tree_inputs(4, K, 3, 128, 128, "f32", 900 + K)
+    x["log_alpha"].zero_()
+    x["beta"].zero_()
+    parents = [[-1] * K] * 4
+    out = kda.tree_fwd(*(x[m] for m in ("q", "k", "v", "log_alpha", "beta", "state")), i32(parents), scale)
+    err = R.rel(out, R.tree(*ref(x), parents, scale))
+    print("relative error", err)
+    assert err <= 8.8e-7
