@@ -105,18 +105,25 @@ struct ScanWork {
     int64_t mapped;                // tokens (over all rows) that the tensor maps cover
 };
 
-// Published words, two channels at once: A, its lowest bit set as the tag of a word that is there
-// (half a step more on A), and B in the high half.  Each word is read and written whole, so a tag
-// comes with its value and nothing else has to be ordered.
+// Published words, two channels at once: the complement of A, whose bits are not all ones (arithmetic makes
+// no such NaN), so that a word of zeros is one that is not there yet, and B in the high half.  Both come
+// back bit for bit: a memory without decay passes thousands of tiles.  Each word is read and written whole,
+// so B comes with its A and nothing else has to be ordered.
 __device__ __forceinline__ void load_words(const unsigned long long* p, unsigned long long& a, unsigned long long& b)
 {
     asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
 }
+__device__ __forceinline__ unsigned long long word_of(float A, float B)
+{
+    return ((unsigned long long)__float_as_uint(B) << 32) | max(~__float_as_uint(A), 1u);
+}
+__device__ __forceinline__ bool word_there(unsigned long long w) { return (unsigned)w != 0; }
+__device__ __forceinline__ float word_A(unsigned long long w) { return __uint_as_float(~(unsigned)w); }
+__device__ __forceinline__ float word_B(unsigned long long w) { return __uint_as_float((unsigned)(w >> 32)); }
 __device__ __forceinline__ void store_words(unsigned long long* p, const float (&A)[2], const float (&B)[2])
 {
-    const unsigned long long a = ((unsigned long long)__float_as_uint(B[0]) << 32) | __float_as_uint(A[0]) | 1u;
-    const unsigned long long b = ((unsigned long long)__float_as_uint(B[1]) << 32) | __float_as_uint(A[1]) | 1u;
-    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(a), "l"(b) : "memory");
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(word_of(A[0], B[0])), "l"(word_of(A[1], B[1]))
+                 : "memory");
 }
 
 // exp of two logarithms of decays, within a half step and little more.  The hardware's exponential is
@@ -536,28 +543,27 @@ __device__ __forceinline__ void await_words(const unsigned long long* p, int64_t
     for (int k = 0; k < N; ++k)
         if (k < count) load_words(p + k * pitch, a[k], b[k]);
     for (int polls = 0;; ++polls) {
-        unsigned long long there = 1;
+        bool there = true;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (k < count) there &= a[k] & b[k];
-        if (__all_sync(0xffffffffu, (int)(there & 1))) return;
+            if (k < count) there = there && word_there(a[k]) && word_there(b[k]);
+        if (__all_sync(0xffffffffu, there)) return;
         if (polls >= kPolls) {
             if (err) atomicOr(err, kErrScanWait);
             return;
         }
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (k < count && !(a[k] & b[k] & 1)) load_words(p + k * pitch, a[k], b[k]);
+            if (k < count && !(word_there(a[k]) && word_there(b[k]))) load_words(p + k * pitch, a[k], b[k]);
     }
 }
 // The run (A, B) followed by a published one.
 __device__ __forceinline__ void append(float (&A)[2], float (&B)[2], unsigned long long a, unsigned long long b)
 {
-    const float pa[2] = {__uint_as_float((unsigned)a), __uint_as_float((unsigned)b)};
-    B[0] = leave(pa[0], __uint_as_float((unsigned)(a >> 32)), B[0]);
-    B[1] = leave(pa[1], __uint_as_float((unsigned)(b >> 32)), B[1]);
-    A[0] = chain(A[0], pa[0]);
-    A[1] = chain(A[1], pa[1]);
+    B[0] = leave(word_A(a), word_B(a), B[0]);
+    B[1] = leave(word_A(b), word_B(b), B[1]);
+    A[0] = chain(A[0], word_A(a));
+    A[1] = chain(A[1], word_A(b));
 }
 
 // A carrier warp: one tile of carry_warps(NS), from tile `from` on.
@@ -603,8 +609,8 @@ __device__ __forceinline__ void scan_carry(const GlrArgs& a, const ScanWork& w, 
             for (int k = 0; k < kBlocks; ++k)
                 if (k < count && k + none > 0) append(pA, pB, v0[k], v1[k]);
             if (none == 0) {
-                carry[0] = __uint_as_float((unsigned)(v0[0] >> 32));
-                carry[1] = __uint_as_float((unsigned)(v1[0] >> 32));
+                carry[0] = word_B(v0[0]);
+                carry[1] = word_B(v1[0]);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

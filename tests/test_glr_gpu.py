@@ -1,6 +1,7 @@
 """Gated linear recurrence on the GPU against the fp64 recurrence, element by element: lengths
 from one token over tile borders to many tiles, packed sequences with empty ones, channel counts
 that no vector divides, pools, strong and no decay, gradients, refusals of the device."""
+import numpy as np
 import pytest
 import torch
 
@@ -232,3 +233,75 @@ def test_rows_behind_the_last_sequence_stay(kda, io, D, end):
     R.within(out[:, :end], H[:, :end], E[:, :end], "out")
     R.within(hT, want, eT, "hT")
     assert bool((out[:, end:] == 5).all())
+
+
+HALF = 2.0 ** -24
+
+
+def long_sums(a, x, first):
+    """h_t = a_t h_{t-1} + x_t of one sequence in fp64, and a bound on its fp32 error that lets no error
+    through that grows with the number of tiles on top of what fp32 decays must cost: every decay is rounded
+    once (its exponential within 1.5 half steps) and meets what stands before it.  Sums and products are
+    folded as a tree: a run's 16 tokens, 4 runs, 8 tiles, 8 blocks, then the carried state through the same and 16
+    tokens, under 120 roundings of partial sums, of which none is above twice the largest |h| so far; the
+    products of decays under 34 in a group of 4096 tokens, which are exact where nothing decays."""
+    h, e = first, np.zeros_like(first)
+    H, E = np.empty_like(x), np.empty_like(x)
+    for t in range(len(x)):
+        e = a[t] * (e + (a[t] != 1) * 1.5 * HALF * np.abs(h))
+        h = a[t] * h + x[t]
+        H[t], E[t] = h, e
+    most = 2 * np.maximum.accumulate(np.maximum(np.abs(H), np.abs(first)), 0)
+    groups = 1 + np.arange(len(x))[:, None] // 4096
+    return H, E + HALF * most * (120 + groups * (1 + 34 * (a != 1).any()))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("least", [0.0, -2e-4])
+@pytest.mark.parametrize("lens,D,packed", [([9001], 8, False), ([70000], 3, False), ([4097, 0, 12288, 600, 33000], 6, True)])
+def test_long_memories(kda, lens, D, packed, least, io):
+    """Decays of 1, or next to it, over many blocks of tiles: forward and backward."""
+    T, N = sum(lens), len(lens)
+    cu, dcu = offsets(lens)
+    g = torch.Generator().manual_seed(T + D)
+    x, dout = (torch.randn((1, T, D), generator=g).to(R.IO[io]) for _ in range(2))
+    la = least * torch.rand((1, T, D), generator=g)
+    h0, dhT = (100 * torch.randn((N, D), generator=g) for _ in range(2))
+    kw = {"cu_seqlens": dcu if packed else None}
+    out, hT, starts = kda.glr_scan_fwd(x.cuda(), la.cuda(), h0=h0.cuda(), output_starts=True, **kw)
+    dx, dla, dh0 = kda.glr_scan_bwd(x.cuda(), la.cuda(), dout.cuda(), starts=starts, h0=h0.cuda(), dhT=dhT.cuda(), **kw)
+    t64 = lambda v: torch.from_numpy(np.ascontiguousarray(v))
+    for n in range(N):
+        s = slice(cu[n], cu[n + 1])
+        if lens[n] == 0:
+            assert torch.equal(hT[n].cpu(), h0[n]) and torch.equal(dh0[n].cpu(), dhT[n])
+            continue
+        a, X, Y = torch.exp(la[0, s].double()).numpy(), R.d(x[0, s]).numpy(), R.d(dout[0, s]).numpy()
+        first, last = h0[n].double().numpy(), dhT[n].double().numpy()
+        H, E = long_sums(a, X, first)
+        R.within(out[0, s], t64(H), t64(E), "out")
+        R.within(hT[n], t64(H[-1]), t64(E[-1]), "hT")
+        # g_t = dout_t + a_{t+1} g_{t+1}: the same sums from the end, with each decay a token later
+        G, EG = long_sums(np.concatenate([np.ones((1, D)), a[:0:-1]]), Y[::-1], last)
+        G, EG = G[::-1], EG[::-1]
+        R.within(dx[0, s], t64(G), t64(EG), "dx")
+        before, eb = np.concatenate([first[None], H[:-1]]), np.concatenate([np.zeros((1, D)), E[:-1]])
+        # the decay of dlog_a = g a h and the two products once more
+        bound = a * (np.abs(before) * EG + np.abs(G) * eb + EG * eb) + 4 * HALF * np.abs(G * a * before)
+        R.within(dla[0, s], t64(G * a * before), t64(bound), "dlog_a")
+        R.within(dh0[n], t64(a[0] * G[0]), t64(a[0] * EG[0] + 4 * HALF * np.abs(G[0])), "dh0")
+
+
+@pytest.mark.parametrize("T,D", [(700, 8), (20000, 5), (131072, 4)])
+def test_a_state_without_decay_stays_as_it_is(kda, T, D):
+    """No decay and no input (padding, a kept state): every product is by 1 and every sum with 0, so the state
+    passes any number of tiles bit for bit, and so do the gradients."""
+    g = torch.Generator().manual_seed(T)
+    zero = torch.zeros(2, T, D, device="cuda")
+    h0, dhT = (torch.randn((2, D), generator=g).cuda() for _ in range(2))
+    out, hT, starts = kda.glr_scan_fwd(zero, zero, h0=h0, output_starts=True)
+    assert torch.equal(hT, h0) and torch.equal(out, h0[:, None].expand_as(out))
+    assert torch.equal(starts, h0[:, None].expand_as(starts))
+    dx, dla, dh0 = kda.glr_scan_bwd(zero, zero, zero, starts=starts, h0=h0, dhT=dhT)
+    assert torch.equal(dh0, dhT) and torch.equal(dx, dhT[:, None].expand_as(dx))
+    assert torch.equal(dla, (dhT * h0)[:, None].expand_as(dla))
