@@ -105,13 +105,22 @@ __device__ __forceinline__ float reciprocal(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-template <typename T> __device__ __forceinline__ float sigmoid(float z);
-template <> __device__ __forceinline__ float sigmoid<float>(float z) { return reciprocal(1.f + expf(-z)); }
-template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float z)
+template <typename T> __device__ __forceinline__ float exponential(float z);
+template <> __device__ __forceinline__ float exponential<float>(float z) { return expf(z); }
+template <> __device__ __forceinline__ float exponential<__nv_bfloat16>(float z)
 {
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    return reciprocal(1.f + e);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * 1.4426950408889634f));
+    return e;
+}
+template <typename T> __device__ __forceinline__ float sigmoid(float z) { return reciprocal(1.f + exponential<T>(-z)); }
+// The sigmoid s and 1 - s, which the slopes need, each to its own last digits: with e = exp(-|z|), which
+// cannot overflow, they are 1 / (1 + e) and e / (1 + e).  (1 - s from a rounded s is 17 % off at z = 15.)
+template <typename T> __device__ __forceinline__ void sigmoids(float z, float& s, float& rest)
+{
+    const float e = exponential<T>(-fabsf(z)), large = reciprocal(1.f + e), small = e * large;
+    s = z >= 0.f ? large : small;
+    rest = z >= 0.f ? small : large;
 }
 
 // Which rows a slot takes.
@@ -270,9 +279,10 @@ group_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ gate,
                 const float t = gate ? z[v][e] : n;
                 float f = t, df = 1.f;
                 if (act != KDA_ACT_NONE) {
-                    const float s = sigmoid<T>(t);
+                    float s, rest;
+                    sigmoids<T>(t, s, rest);
                     f = act == KDA_ACT_SILU ? t * s : s;
-                    df = s + (act == KDA_ACT_SILU ? f : -s) * (act == KDA_ACT_SILU ? 1.f - s : s);
+                    df = act == KDA_ACT_SILU ? s + f * rest : s * rest;
                 }
                 const float dn = y[v][e] * (gate ? f : df);
                 z[v][e] = y[v][e] * n * df;      // dgate

@@ -116,3 +116,40 @@ def test_no_rows(kda):
     assert dx.shape == (0, 4, 64) and float(dw.abs().sum()) == 0 and float(db.abs().sum()) == 0
     x = torch.zeros(3, 0, 64, device="cuda")
     assert kda.group_norm_fwd(x, w).shape == (3, 0, 64)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["sigmoid", "silu"])
+@pytest.mark.parametrize("low,high", [(8.0, 20.0), (-20.0, -8.0), (-1.0, 1.0)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_slopes_of_open_and_shut_gates(kda, gated, low, high, name, io):
+    """Gradients through the flat parts of the activation, relative to the slope there.  An error of the slope: the
+    exponential's (with its argument's, for bf16 I/O, |t| + 4 half steps; 4 for fp32), 1 + e, the
+    reciprocal's, three products: under 40 half steps for |t| <= 21, which ROW, 64, covers.  n, where it
+    is the argument, is off by ROW of what it is made of, and the slope by that share more."""
+    M, G, d = 50, 3, 64
+    x, _, w, b, dy = inputs(M, G, d, io, False, 77)
+    g = torch.Generator().manual_seed(5)
+    z = (low + (high - low) * torch.rand((M, G, d), generator=g)).to(R.IO[io]).cuda() if gated else None
+    if not gated:                        # n in [low, high] but for a few outliers
+        w, b = w * (high - low) / 8, b * 0 + (low + high) / 2
+    kw = dict(eps=EPS, activation=name)
+    got = kda.group_norm_bwd(x, w, dy, bias=b, gate=z, **kw)
+    want = R.grads(lambda x, w, b, z: R.group_norm(x, w, b, z, EPS, name, False), [R.d(t) for t in (x, w, b, z)], R.d(dy))
+    X, W, Y = R.d(x), R.d(w), R.d(dy)
+    r = 1 / torch.sqrt((X ** 2).mean(-1, keepdim=True) + EPS)
+    big = X.abs() * r * (1 + (X.abs() * r).mean(-1, keepdim=True))
+    n, nb = X * r * W + R.d(b), big * W.abs() + R.d(b).abs()
+    t = R.d(z) if gated else n
+    s = torch.sigmoid(t)
+    rest = torch.sigmoid(-t)
+    slope = s * rest if name == "sigmoid" else s * (1 + t.abs() * rest)      # the magnitudes that SiLU's sums
+    f = R.act(name, t).abs()
+    dn = Y.abs() * (f if gated else slope * (1 + 2 * nb))                    # (its own slope is below 2 of it)
+    if gated:
+        R.within(got[1], want[3], 2 * R.ROW * Y.abs() * nb * slope, "dgate")
+    c = dn * W.abs()
+    R.within(got[0], want[0], 4 * R.ROW * r * (c + big * (c * big).mean(-1, keepdim=True)) * (1 + big), "dx")
+    steps = 8 * R.ROW + (M * G + 64) * 2.0 ** -24
+    R.within(got[2], want[1], steps * (dn * big).sum((0, 1)), "dweight")
+    R.within(got[3], want[2], steps * dn.sum((0, 1)), "dbias")
