@@ -672,8 +672,10 @@ def group_norm_bwd(x, weight, dout, bias=None, gate=None, eps=1e-5, activation="
     _check(dout, "dout", x.dtype, x.shape, x.device)
     dx = torch.empty_like(x)
     dgate = torch.empty_like(x) if gate is not None else None
-    dweight = torch.empty_like(weight) if weight is not None else None
-    dbias = torch.empty_like(bias) if bias is not None else None
+    # without heads the call writes nothing, and weights that heads would share have gradients still
+    fresh = torch.empty_like if G > 0 else torch.zeros_like
+    dweight = fresh(weight) if weight is not None else None
+    dbias = fresh(bias) if bias is not None else None
     _call("kda_group_norm_bwd", x.device, x.data_ptr(), _addr(gate), _addr(weight), _addr(bias),
           dout.data_ptr(), dx.data_ptr(), _addr(dgate), _addr(dweight), _addr(dbias), M, G, d,
           per_group, 1 if center else 0, float(eps), _ACT[activation], io)

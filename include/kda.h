@@ -529,7 +529,8 @@ KDA_API kda_status_t kda_tree_commit(const void* k, const void* v, const float* 
  *   when gate is given) in io_dtype; dweight, dbias fp32 in the layout of weight and
  *   bias, or NULL if not wanted (dweight is also defined for weight NULL).  The sums over tokens
  *   are fp32, in a fixed order (the same result on every run), through a workspace
- *   of at most 16 MB, or twice the size of weight and bias gradients where that is more.  M = 0 sets dweight and dbias to zero.
+ *   of at most 16 MB, or twice the size of weight and bias gradients where that is more.  M = 0 sets
+ *   dweight and dbias to zero; G = 0 writes nothing, not those of shared weights either.
  */
 typedef enum {
     KDA_ACT_NONE = 0,

@@ -153,3 +153,16 @@ def test_slopes_of_open_and_shut_gates(kda, gated, low, high, name, io):
     steps = 8 * R.ROW + (M * G + 64) * 2.0 ** -24
     R.within(got[2], want[1], steps * (dn * big).sum((0, 1)), "dweight")
     R.within(got[3], want[2], steps * dn.sum((0, 1)), "dbias")
+
+
+def test_no_heads(kda):
+    """Without heads the gradients of weights that they share are zero, not what the memory held."""
+    for k in range(4):
+        torch.full((64,), float("nan"), device="cuda")                # what a fresh tensor is made of next
+        w = torch.ones(64, device="cuda")
+        torch.full((64,), float("nan"), device="cuda")
+        x = torch.zeros(3, 0, 64, device="cuda")
+        dx, dz, dw, db = kda.group_norm_bwd(x, w, x, bias=w, gate=x)
+        assert dx.shape == dz.shape == (3, 0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
+        w = torch.ones(0, 64, device="cuda")
+        assert kda.group_norm_bwd(x, w, x)[2].shape == (0, 64)
