@@ -429,9 +429,6 @@ def gdn_chunk_bwd(q, k, v, log_a, beta, scale, dout, h0=None, dhT=None, cu_seqle
                      need_dh0=need_dh0, _gdn=True)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's address, by device index
-
-
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -443,11 +440,13 @@ def _call(name, dev, *args):
     if index is None or dev.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a CUDA device, not {dev}")
     fn = getattr(_lib or _load(), name)
+    # the current stream's address; builds of torch without CUDA do not have the name
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
-        st = fn(*args, _raw_stream(index))
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(index))
+            st = fn(*args, stream)
     if st != KDA_OK:
         raise KDAError(st, name)
 

@@ -216,3 +216,23 @@ def test_tree_formula_against_one_path():
             err = x["beta"][0, j][:, None] * (x["v"][0, j] - (x["k"][0, j][:, :, None] * S).sum(1))
             S = S + x["k"][0, j][:, :, None] * err[:, None]
         torch.testing.assert_close(out[0, i], scale * (x["q"][0, i][:, :, None] * S).sum(1))
+
+
+def test_import_without_cuda_in_torch():
+    """The package and its modules import where torch was built without CUDA (names of its CUDA bindings are
+    missing there); only calls raise."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import sys; sys.path.insert(0, %r)\n"
+            "import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import gated_delta_rule_75_b200 as kda\n"
+            "import gated_delta_rule_75_b200.context_parallel\n"
+            "x = torch.zeros(1, 4, 8)\n"
+            "try:\n    kda.glr_scan_fwd(x, x)\n"
+            "except ValueError as e:\n    assert 'CUDA device' in str(e)\n    print('raised')\n" % root)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "raised" in r.stdout, r.stderr[-1500:]
