@@ -89,12 +89,13 @@ struct Divide {
 };
 
 // Workspace: for every group its entry state and the (A, B) of its blocks but the last, which the next
-// group's entry state holds, side by side so that one wait asks for them together; the tiles' (A, B). All
-// zeroed by the setup kernel; with cu_seqlens each tile's range of offsets.  A column is one block of kCh
+// group's entry state holds, side by side so that one wait asks for them together (a row of words for
+// every block; none for a single one, which nothing crosses); the tiles' (A, B).  All zeroed by
+// the setup kernel; with cu_seqlens each tile's range of offsets.  A column is one block of kCh
 // channels of one row of the token axis; tiles, blocks and groups are numbered in the order of
 // the scan (from the end in the backward).
 struct ScanWork {
-    unsigned long long* groups;    // [groups][kBlocks][cols][kCh]: words (1, entry state), then (A, B) of blocks
+    unsigned long long* groups;    // [blocks][cols][kCh]: of a group words (1, entry state), then (A, B) of blocks
     unsigned long long* tile_ab;   // [tiles][cols][kCh]: words (A, B)
     int2* range;                   // [tiles]: offsets cu[x .. y - 1] lie in [first token, first + kTile]
     int64_t cols, tiles, total;    // total = tiles * cols
@@ -833,14 +834,14 @@ cudaError_t launch_scan(const GlrArgs& a, cudaStream_t st)
     // a single tile per column waits for nothing: no setup, unless offsets or sequences without
     // tokens want looking at
     if (w.tiles > 1 || a.cu || a.T == 0) {
-        const int64_t blocks = (w.tiles + kBlock - 1) / kBlock, groups = (blocks + kBlocks - 1) / kBlocks;
-        const int64_t words = (groups * kBlocks * w.cols + w.total) * kCh, ranges = (w.tiles + 1) / 2 * 2;
+        const int64_t blocks = (w.tiles + kBlock - 1) / kBlock, rows = blocks > 1 ? blocks : 0;
+        const int64_t words = w.tiles > 1 ? (rows * w.cols + w.total) * kCh : 0, ranges = a.cu ? (w.tiles + 1) / 2 * 2 : 0;
         const cudaError_t e = buf.alloc((size_t)((words + ranges) * 8), st);
         if (e != cudaSuccess) return e;
         w.groups = static_cast<unsigned long long*>(buf.ptr);
-        w.tile_ab = w.groups + groups * kBlocks * w.cols * kCh;
-        w.range = reinterpret_cast<int2*>(w.tile_ab + w.total * kCh);
-        w.zeroed = w.tiles > 1 ? words / 2 : 0;
+        w.tile_ab = w.groups + rows * w.cols * kCh;
+        w.range = reinterpret_cast<int2*>(w.groups + words);
+        w.zeroed = words / 2;
         const int64_t work = w.zeroed / 8 + (a.cu ? w.tiles : 0) + (a.cu || a.T == 0 ? a.N * 256 : 0);
         const int64_t ctas = (work + 255) / 256;
         LaunchScope scope(st, K_GLR_SETUP);

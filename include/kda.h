@@ -424,9 +424,10 @@ KDA_API kda_status_t kda_affine_prefix(const float* maps, const float* offs, con
  *              their rows of out (dx, dlog_a in the backward) left as they were.
  * Any D >= 1 up to 2^20, fewer than 2^31 - 128 tokens in all; D, B or T of 0 is a no-op
  * apart from hT = h0.  The state is fp32 throughout; out is
- * rounded once.  A call over more than one tile of the token axis uses a workspace of
- * about 10 bytes per tile and channel from the library's pool.  The result is the same
- * on every run.
+ * rounded once.  A call over more than one tile of the token axis uses a workspace
+ * from the library's pool: 8 bytes per tile and channel, 8 more per 8 tiles and channel where there
+ * are more than 8 (channels in whole 64s), and 8 per tile with cu_seqlens.  The result is the
+ * same on every run.
  *
  * kda_glr_scan_fwd_slots -- h0 = hT = state_pool[slots[n]] ([P, D] fp32), with the
  *   rules of kda_chunk_fwd_slots: a negative slot starts from zero and stores nothing,

@@ -305,3 +305,19 @@ def test_a_state_without_decay_stays_as_it_is(kda, T, D):
     dx, dla, dh0 = kda.glr_scan_bwd(zero, zero, zero, starts=starts, h0=h0, dhT=dhT)
     assert torch.equal(dh0, dhT) and torch.equal(dx, dhT[:, None].expand_as(dx))
     assert torch.equal(dla, (dhT * h0)[:, None].expand_as(dla))
+
+
+@pytest.mark.parametrize("B,T,D,packed", [(64, 128, 4096, False), (64, 100, 1000, False), (1, 2000, 4096, True),
+                                          (16, 512, 2048, False), (16, 513, 2048, False), (2, 64 * 71, 2048, False)])
+def test_workspace_is_what_the_header_says(kda, B, T, D, packed):
+    x, la = torch.zeros(B, T, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, T, D, device="cuda")
+    _, dcu = offsets([T // 2, T - T // 2])
+    h0 = torch.randn(2 if packed else B, D, device="cuda")
+    kda.workspace_high_water(reset=True)
+    out, hT = kda.glr_scan_fwd(x, la, h0=h0, cu_seqlens=dcu if packed else None)
+    used = kda.workspace_high_water()
+    tiles, channels = -(-T // 64), B * (-(-D // 64) * 64)
+    blocks = -(-tiles // 8)
+    says = 8 * tiles * channels + (8 * blocks * channels if blocks > 1 else 0) + (8 * (tiles + 1) if packed else 0)
+    assert used <= says + 4096                            # the pool's own rounding
+    assert torch.equal(hT, h0)
