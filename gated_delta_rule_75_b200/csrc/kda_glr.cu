@@ -265,7 +265,7 @@ struct Stage {
     int marked;                                                  // whether first / last hold anything
     int plain;                                                   // no marks, all tokens there and in the maps
     int folded;                                                  // runs that are there
-    uint64_t taken, full, agg, carried, empty;
+    uint64_t taken, full, agg, carried, empty;                   // full: the copies, and the loader's notes
     static constexpr uint32_t kCopied = kTile * (La::kPitch + X::kPitch * (Bwd ? 2 : 1));
 
     __device__ __forceinline__ int la_at(int r) const { return Mode == kWhole ? r * La::kPitch : off[r] & 0xffff; }
@@ -275,6 +275,17 @@ template <typename T, int Mode, bool Bwd> constexpr int ring_stages()
 {
     constexpr int n = (int)((227 * 1024 - 64) / sizeof(Stage<T, Mode, Bwd>));
     return n < 8 ? n : 8;
+}
+
+// A worker's wait for its tile q in stage q % NS.  A barrier tells phases apart by their parity alone, so a
+// wait may only begin once the phase before has ended; copies land in any order, and a group that takes
+// every third tile may be done with tile q - 3 while tile q - NS is still on its way to the stage.  The loader
+// goes in order: the wait for `taken` may begin once tile q - NS was taken, which the worker's last tile, a later one,
+// shows, and it ends after tile q - NS has left the stage, which ends its phase of `full`.
+template <typename S>
+__device__ __forceinline__ bool await_tile(S& s, uint32_t parity, int* err)
+{
+    return umma::mbar_wait(&s.taken, parity, err, kScanBit) && umma::mbar_wait(&s.full, parity, err, kScanBit) && s.id >= 0;
 }
 
 // Where a tile lies (tiles, columns and their product fit 31 bits).
@@ -432,7 +443,7 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
     const int64_t used = tokens_used(a);
     for (int64_t q = group;; q += agg_groups(Bwd)) {
         S& s = ring[q % NS];
-        if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
+        if (!await_tile(s, (uint32_t)((q / NS) & 1), a.err)) return;
         const TileAt at(a, w, s.id, Bwd);
         F2 A(1.f, 1.f), B(0.f, 0.f);
         if (s.plain) {
@@ -641,7 +652,7 @@ __device__ __forceinline__ void scan_finish(const GlrArgs& a, const ScanWork& w,
     const int64_t used = tokens_used(a);
     for (int64_t q = group;; q += kFinGroups) {
         S& s = ring[q % NS];
-        if (!umma::mbar_wait(&s.full, (uint32_t)((q / NS) & 1), a.err, kScanBit) || s.id < 0) return;
+        if (!await_tile(s, (uint32_t)((q / NS) & 1), a.err)) return;
         const TileAt at(a, w, s.id, Bwd);
         const int live = (int)(used - at.t0 < kTile ? used - at.t0 : kTile);     // tokens that exist (or less than none)
         const int64_t c = at.c0 + (Mode != kSingle ? 2 * lane : lane);

@@ -321,3 +321,29 @@ def test_workspace_is_what_the_header_says(kda, B, T, D, packed):
     says = 8 * tiles * channels + (8 * blocks * channels if blocks > 1 else 0) + (8 * (tiles + 1) if packed else 0)
     assert used <= says + 4096                            # the pool's own rounding
     assert torch.equal(hT, h0)
+
+
+@pytest.mark.parametrize("io,B,T,D", [("bf16", 1024, 65, 4096), ("bf16", 700, 66, 4094), ("bf16", 300, 129, 4093),
+                                      ("f32", 512, 65, 4096), ("f32", 400, 67, 2046)])
+def test_many_short_rows(kda, io, B, T, D):
+    """Tiles that take a worker next to no time, so that workers run as far ahead of the copies as the ring
+    lets them: every one of many calls ends well, with the same result, which is the recurrence's."""
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    x = torch.randn((B, T, D), generator=g, device="cuda").to(R.IO[io])
+    la = torch.rand((B, T, D), generator=g, device="cuda").mul_(-0.2)
+    h0 = torch.randn((B, D), generator=g, device="cuda")
+    out, hT, starts = kda.glr_scan_fwd(x, la, h0=h0, output_starts=True)
+    h, m, e = h0.double(), h0.double().abs(), torch.zeros_like(h0, dtype=torch.float64)
+    for t in range(T):                                    # the bound of operators_ref.glr
+        a, y = torch.exp(la[:, t].double()), x[:, t].double()
+        h, m = a * h + y, a * m + y.abs()
+        e = a * e + R.STEP * m
+        assert bool(((out[:, t].double() - h).abs() <= e + R.HALF_STEP[x.dtype] * (h.abs() + e)).all()), t
+    assert bool(((hT.double() - h).abs() <= e + R.HALF_STEP[torch.float32] * (h.abs() + e)).all())
+    again = torch.empty_like(out)
+    grads = kda.glr_scan_bwd(x, la, x, starts=starts, h0=h0, dhT=h0)
+    for _ in range(25):
+        kda.glr_scan_fwd(x, la, h0=h0, out=again, hT=hT)
+        assert torch.equal(out, again)
+    for _ in range(10):
+        assert all(torch.equal(p, q) for p, q in zip(grads, kda.glr_scan_bwd(x, la, x, starts=starts, h0=h0, dhT=h0)))
