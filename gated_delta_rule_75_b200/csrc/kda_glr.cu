@@ -524,6 +524,7 @@ __device__ __forceinline__ void scan_aggregate(const GlrArgs& a, const ScanWork&
             __threadfence_block();
         }
         if (__shfl_sync(0xffffffffu, before, 0) == kRuns - 1) {
+            __syncwarp();                        // what lane 0 has seen of the other runs holds for all lanes
             float tA[2] = {1.f, 1.f}, tB[2] = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kRuns; ++k) {

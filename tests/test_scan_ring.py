@@ -146,3 +146,12 @@ def test_the_kernel_waits_as_the_model_does():
         assert "await_tile(" in body and "s.full" not in body, role
     carry = re.search(r"void scan_carry\(.*?\n\}\n", code, re.S).group(0)
     assert carry.index("s.taken") < carry.index("s.agg") and "s.full" not in carry
+
+
+def test_the_fold_reads_the_other_runs_in_order():
+    """Lane 0 alone counts the runs that are there; a shuffle hands the count on but orders no memory, so the
+    lanes that read the other runs meet at __syncwarp() first."""
+    with open(os.path.join(CSRC, "kda_glr.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    fold = re.search(r"__shfl_sync\([^)]*before, 0\) == kRuns - 1\) \{(.*?)s\.A\[", code, re.S).group(1)
+    assert fold.lstrip().startswith("__syncwarp();")
