@@ -42,8 +42,8 @@
 // the tile from its kept entry state (starts), so the pass reads x, log_a, dout and
 // writes dx, dlog_a once.
 //
-// Measured (copies run at 6.46 TB/s): 8 x 8192 x 4096 bf16, 2.15 GB, 400 us when the SM clock is at
-// its top and 440 under the power cap (1660 MHz); 131071 x 1024 fp32, 1.61 GB, 293 us; 8 x 8192 x
+// Measured (copies run at 6.46 TB/s): 8 x 8192 x 4096 bf16, 2.15 GB, 380 us when the SM clock is at
+// its top and 440 under the power cap (1660 MHz); 131071 x 1024 fp32, 1.61 GB, 293 us (316); 8 x 8192 x
 // 4096 in registers, a CTA a tile, 644.  Tiles of 64 x 64: their ring (8 stages of 28 KiB for bf16)
 // keeps about 190 KiB of an SM on its way or in work for the 5 us from a tile's copy to its last store.
 #include "kda_common.cuh"
@@ -62,7 +62,7 @@ constexpr int kBlock = 8;               // tiles of a block
 constexpr int kBlocks = 8;              // blocks of a group
 static_assert(kBlocks <= kBlock, "words of a group and of a block are held in the same registers");
 constexpr int kPolls = 1 << 21;         // about two seconds of polling
-constexpr int kScanBit = 7;             // kErrScanWait
+constexpr int kScanBit = 7;             // kErrScanWait; its waits are a whole warp's, 4 us a poll, so 80 ms in all
 
 // Warps by role.
 constexpr int kFinGroups = 2, kFinWarps = kFinGroups * kRuns;

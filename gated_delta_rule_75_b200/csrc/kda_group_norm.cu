@@ -18,7 +18,7 @@
 // there are more heads than slots in a CTA) leaves in the workspace for a second kernel to add
 // in a fixed order: the gradients are the same on every run.  Bound by memory: forward 65536 x 32 x 128
 // bf16, 1.61 GB, 267 us (6.0 TB/s); backward 20011 x 16 x 128 fp32, 0.82 GB, 150 us (5.5 TB/s, 4 of them
-// the second kernel).
+// the second kernel), 65536 x 32 x 128 bf16, 2.68 GB, 527 us (5.1 TB/s: the same arithmetic for half the bytes).
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -440,7 +440,7 @@ cudaError_t norm_bwd(const GroupNormArgs& a, cudaStream_t st)
 
 // F(NV, LPG) for rows of `vecs` vectors of VEC elements, at least LEAST vectors a lane.  The forward takes two
 // where a vector is 8 bytes (20000 x 13 x 100 bf16: 50 -> 45 us); the backward has enough in work
-// with one (30000 x 10 x 100: 103 us, 112 with two).
+// with one (30000 x 10 x 100 bf16: 108 us, 114 with two).
 #define KDA_NORM_BY_VECS(F, T, VEC, LEAST)                                      \
     do {                                                                       \
         constexpr int NV = VEC * sizeof(T) == 16 ? 1 : LEAST;                   \
